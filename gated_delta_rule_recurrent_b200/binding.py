@@ -16,7 +16,8 @@ from typing import Optional, Tuple
 import torch
 
 __all__ = ["decode", "decode_gated", "prefill", "prefill_gated", "linear_attention_gate",
-           "device_error", "GdrError", "lib",
+           "linear_attention_decode", "linear_attention_prefill", "state_quantize",
+           "state_dequantize", "device_error", "GdrError", "lib",
            "library_path", "last_launch", "kernel_forms", "KERNEL_NAMES",
            "STATUS_NAMES", "Dims", "LaunchInfo"]
 
@@ -55,7 +56,8 @@ class LaunchInfo(ctypes.Structure):
 
 # gdr_kernel values of include/gdr.h
 KERNEL_NAMES = {0: "none", 1: "single_token", 2: "chunked", 3: "tensor_core",
-                4: "tensor_core_one", 5: "gate", 6: "prefill", 7: "rows"}
+                4: "tensor_core_one", 5: "gate", 6: "prefill", 7: "rows", 8: "linear_decode",
+                9: "linear_prefill", 10: "state_cache"}
 
 _P = ctypes.c_void_p
 _DECODE_ARGTYPES = [ctypes.POINTER(Dims), _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
@@ -100,6 +102,16 @@ def lib() -> ctypes.CDLL:
         L.gdr_linear_attention_gate.argtypes = [P, P, P, P, P, P, ctypes.c_int64, ctypes.c_int32,
                                                 ctypes.c_int, P]
         L.gdr_linear_attention_gate.restype = ctypes.c_int
+        D, I = ctypes.POINTER(Dims), ctypes.c_int32
+        L.gdr_linear_attention_decode.argtypes = [D, P, P, P, P, P, P, P, P, ctypes.c_float, P, P]
+        L.gdr_linear_attention_decode.restype = ctypes.c_int
+        L.gdr_linear_attention_prefill.argtypes = [D, P, P, P, P, P, P, P, ctypes.c_float, P, P]
+        L.gdr_linear_attention_prefill.restype = ctypes.c_int
+        L.gdr_state_quantize.argtypes = [P, I, P, P, P, I, P, I, ctypes.c_int64, ctypes.c_int, P]
+        L.gdr_state_quantize.restype = ctypes.c_int
+        L.gdr_state_dequantize.argtypes = [P, P, I, P, P, I, P, I, ctypes.c_int64, ctypes.c_int,
+                                           P]
+        L.gdr_state_dequantize.restype = ctypes.c_int
         L.gdr_last_launch.argtypes = [ctypes.POINTER(LaunchInfo)]
         L.gdr_last_launch.restype = ctypes.c_int
         L.gdr_kernel_form_count.argtypes = []
@@ -135,7 +147,7 @@ def last_launch() -> dict:
 
 
 def kernel_forms() -> list:
-    """Every decode kernel form the dispatcher can choose (``gdr_kernel_form``),
+    """Every gated-delta-rule kernel form the dispatcher can choose (``gdr_kernel_form``),
     as dicts with kernel, D_k, tile_cols, gated and layout. Needs no GPU."""
     L = lib()
     forms = []
@@ -370,3 +382,157 @@ def linear_attention_gate(a: torch.Tensor, dt_bias: torch.Tensor, decay_scale: t
             _ptr(decay), _ptr(beta), rows, H, _GATE_DTYPES[a.dtype], ctypes.c_void_p(stream))
     _check(rc)
     return decay, beta
+
+
+def _linear_args(query, key, value, log_decay, state_pool, actual_seq_lengths,
+                 ssm_state_indices, num_accepted_tokens, out):
+    if not isinstance(query, torch.Tensor) or query.dim() != 4:
+        raise RuntimeError("query must be a 4-D tensor [B, H_qk, T, D_k]")
+    device = query.device
+    if device.type != "cuda":
+        raise RuntimeError("all tensors must be on a CUDA device")
+    if not isinstance(value, torch.Tensor) or value.dim() != 4:
+        raise RuntimeError("value must be a 4-D tensor [B, H_v, T, D_v]")
+    if not isinstance(state_pool, torch.Tensor) or state_pool.dim() != 4:
+        raise RuntimeError("state_pool must be a 4-D tensor [pool, H_v, D_k, D_v]")
+    B, H_qk, T, D_k = query.shape
+    H_v, D_v = value.shape[1], value.shape[3]
+    bf16, i32 = torch.bfloat16, torch.int32
+    _need(query, "query", bf16, (B, H_qk, T, D_k), device)
+    _need(key, "key", bf16, (B, H_qk, T, D_k), device)
+    _need(value, "value", bf16, (B, H_v, T, D_v), device)
+    _need(log_decay, "log_decay", torch.float32, (H_v,), device)
+    _need(state_pool, "state_pool", bf16, (state_pool.shape[0], H_v, D_k, D_v), device)
+    _need(actual_seq_lengths, "actual_seq_lengths", i32, (B,), device)
+    _need(ssm_state_indices, "ssm_state_indices", i32, (B,), device)
+    if num_accepted_tokens is not None:
+        _need(num_accepted_tokens, "num_accepted_tokens", i32, (B,), device)
+    if out is None:
+        out = torch.empty((B, H_v, T, D_v), dtype=bf16, device=device)
+    else:
+        _need(out, "out", bf16, (B, H_v, T, D_v), device)
+    dims = Dims(B, T, H_qk, H_v, D_k, D_v, state_pool.shape[0], 0)
+    return device, dims, out
+
+
+def linear_attention_decode(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
+                            log_decay: torch.Tensor, state_pool: torch.Tensor,
+                            actual_seq_lengths: torch.Tensor, ssm_state_indices: torch.Tensor,
+                            num_accepted_tokens: Optional[torch.Tensor] = None,
+                            scale_value: float = 1.0, *,
+                            out: Optional[torch.Tensor] = None
+                            ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Linear attention with one decay per head for one to eight tokens, through
+    ``gdr_linear_attention_decode``: S = S * exp(log_decay[h]) + k v^T, then
+    o = S^T (q * scale_value), token by token.
+
+    ``log_decay`` is [H_v] float32; every other argument, and the in-place
+    update of ``state_pool`` (the second result), as for ``decode``. Queued on
+    the current CUDA stream; no synchronisation.
+    """
+    device, dims, out = _linear_args(query, key, value, log_decay, state_pool,
+                                     actual_seq_lengths, ssm_state_indices,
+                                     num_accepted_tokens, out)
+    with torch.cuda.device(device):
+        stream = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+        rc = lib().gdr_linear_attention_decode(
+            ctypes.byref(dims), _ptr(query), _ptr(key), _ptr(value), _ptr(log_decay),
+            _ptr(state_pool), _ptr(actual_seq_lengths), _ptr(ssm_state_indices),
+            _ptr(num_accepted_tokens), float(scale_value), _ptr(out), stream)
+    _check(rc)
+    return out, state_pool
+
+
+def linear_attention_prefill(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
+                             log_decay: torch.Tensor, state_pool: torch.Tensor,
+                             actual_seq_lengths: torch.Tensor, ssm_state_indices: torch.Tensor,
+                             scale_value: float = 1.0, *, out: Optional[torch.Tensor] = None
+                             ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The recurrence of ``linear_attention_decode`` over prompts of any length,
+    through ``gdr_linear_attention_prefill`` (chunks of 128 tokens on the tensor
+    cores). All valid tokens are committed. Queued on the current CUDA stream;
+    no synchronisation.
+    """
+    device, dims, out = _linear_args(query, key, value, log_decay, state_pool,
+                                     actual_seq_lengths, ssm_state_indices, None, out)
+    with torch.cuda.device(device):
+        stream = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+        rc = lib().gdr_linear_attention_prefill(
+            ctypes.byref(dims), _ptr(query), _ptr(key), _ptr(value), _ptr(log_decay),
+            _ptr(state_pool), _ptr(actual_seq_lengths), _ptr(ssm_state_indices),
+            float(scale_value), _ptr(out), stream)
+    _check(rc)
+    return out, state_pool
+
+
+# gdr_cache_type values of include/gdr.h
+_CACHE_TYPES = {torch.int8: 0, torch.float8_e4m3fn: 1}
+_CACHE_GROUP = 64
+
+
+def _cache_args(state_pool, ssm_state_indices, cache, scales, cache_indices):
+    for t, name in ((state_pool, "state_pool"), (cache, "cache")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise RuntimeError(f"{name} must be a 4-D tensor ([pool or entries, H_v, rows, "
+                               "columns])")
+    device = state_pool.device
+    if device.type != "cuda":
+        raise RuntimeError("all tensors must be on a CUDA device")
+    P, H, R, C = state_pool.shape
+    N = cache.shape[0]
+    if cache.dtype not in _CACHE_TYPES:
+        raise RuntimeError(f"cache must be int8 or float8_e4m3fn, got {cache.dtype}")
+    if C % _CACHE_GROUP != 0:
+        raise RuntimeError("state_pool's last axis must be a multiple of 64")
+    if not isinstance(ssm_state_indices, torch.Tensor) or ssm_state_indices.dim() != 1:
+        raise RuntimeError("ssm_state_indices must be a 1-D tensor")
+    n = ssm_state_indices.shape[0]
+    _need(state_pool, "state_pool", torch.bfloat16, (P, H, R, C), device)
+    _need(cache, "cache", cache.dtype, (N, H, R, C), device)
+    _need(scales, "scales", torch.float32, (N, H, R, C // _CACHE_GROUP), device)
+    _need(ssm_state_indices, "ssm_state_indices", torch.int32, (n,), device)
+    _need(cache_indices, "cache_indices", torch.int32, (n,), device)
+    return device, P, N, n, H * R * C, _CACHE_TYPES[cache.dtype]
+
+
+def state_quantize(state_pool: torch.Tensor, ssm_state_indices: torch.Tensor,
+                   cache: torch.Tensor, scales: torch.Tensor, cache_indices: torch.Tensor
+                   ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Write slots of a state pool to an 8-bit cache through ``gdr_state_quantize``:
+    slot ``ssm_state_indices[i]`` to entry ``cache_indices[i]`` (both [n] int32,
+    entries distinct; a pair outside its range is skipped).
+
+    ``state_pool`` is [pool, H_v, D_k, D_v] or [pool, H_v, D_v, D_k] bfloat16,
+    ``cache`` [entries, ...] of the same slot shape in int8 or float8_e4m3fn,
+    ``scales`` [entries, H_v, rows, columns / 64] float32: 64 consecutive
+    values share a scale. Returns (cache, scales). Queued on the current CUDA
+    stream; no synchronisation.
+    """
+    device, P, N, n, values, kind = _cache_args(state_pool, ssm_state_indices, cache, scales,
+                                                cache_indices)
+    with torch.cuda.device(device):
+        stream = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+        rc = lib().gdr_state_quantize(_ptr(state_pool), P, _ptr(ssm_state_indices), _ptr(cache),
+                                      _ptr(scales), N, _ptr(cache_indices), n, values, kind,
+                                      stream)
+    _check(rc)
+    return cache, scales
+
+
+def state_dequantize(cache: torch.Tensor, scales: torch.Tensor, cache_indices: torch.Tensor,
+                     state_pool: torch.Tensor, ssm_state_indices: torch.Tensor) -> torch.Tensor:
+    """Read entries of an 8-bit cache back into slots of a state pool through
+    ``gdr_state_dequantize``: entry ``cache_indices[i]`` to slot
+    ``ssm_state_indices[i]`` (slots distinct; one entry may go to several slots).
+    The tensors are those of ``state_quantize``. Returns ``state_pool``, updated
+    in place. Queued on the current CUDA stream; no synchronisation.
+    """
+    device, P, N, n, values, kind = _cache_args(state_pool, ssm_state_indices, cache, scales,
+                                                cache_indices)
+    with torch.cuda.device(device):
+        stream = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+        rc = lib().gdr_state_dequantize(_ptr(cache), _ptr(scales), N, _ptr(cache_indices),
+                                        _ptr(state_pool), P, _ptr(ssm_state_indices), n, values,
+                                        kind, stream)
+    _check(rc)
+    return state_pool

@@ -1,13 +1,15 @@
 """Build libgdr.so in-tree with nvcc for sm_100a.
 
 ``python -m gated_delta_rule_recurrent_b200.build`` compiles
-``csrc/gdr_api.cu`` (which includes the kernel header) into
-``gated_delta_rule_recurrent_b200/libgdr.so``. A sidecar file records a hash
-of every source and of the command, so ``ensure_built()`` rebuilds exactly
-when something changed (file times are not trusted across copies).
+``csrc/gdr_api.cu`` and ``csrc/gdr_linear_api.cu`` (which include the kernel
+headers) into objects and links them into
+``gated_delta_rule_recurrent_b200/libgdr.so``. Sidecar files record a hash of
+the sources and of the flags, so ``ensure_built()`` rebuilds exactly what
+changed (file times are not trusted across copies).
 """
 from __future__ import annotations
 
+import concurrent.futures
 import hashlib
 import os
 import shutil
@@ -26,16 +28,23 @@ HASH_PATH = LIB_PATH + ".srchash"
 TEST_HOOKS_LIB_PATH = os.path.join(PKG_DIR, "libgdr_testhooks.so")
 TEST_HOOKS_FLAGS = ["-DGDR_TEST_HOOKS"]
 
-SOURCES = [os.path.join(CSRC, "gdr_api.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, name) for name in (
-    "gdr_decode.cuh", "gdr_ptx.cuh", "gdr_decode_tma.cuh", "gdr_decode_chunk.cuh", "gdr_decode_chunk_tc.cuh",
-    "gdr_decode_rows.cuh",
-    "gdr_umma.cuh", "gdr_gate.cuh", "gdr_prefill_tc.cuh")] + [
+_COMMON = [os.path.join(CSRC, name) for name in (
+    "gdr_decode.cuh", "gdr_host.h", "gdr_ptx.cuh", "gdr_umma.cuh")] + [
     os.path.join(INCLUDE, "gdr.h")]
+# Each source with the files it is compiled from, itself first.
+UNITS = {os.path.join(CSRC, source): [os.path.join(CSRC, name) for name in (source, *headers)]
+         + _COMMON for source, headers in (
+    ("gdr_api.cu", ("gdr_decode_tma.cuh", "gdr_decode_chunk.cuh", "gdr_decode_chunk_tc.cuh",
+                    "gdr_decode_rows.cuh", "gdr_gate.cuh", "gdr_prefill_tc.cuh")),
+    ("gdr_linear_api.cu", ("gdr_linear.cuh", "gdr_linear_decode.cuh", "gdr_linear_prefill.cuh",
+                           "gdr_state_cache.cuh")))}
+SOURCES = list(UNITS)
+DEPS = list(dict.fromkeys(path for files in UNITS.values() for path in files))
+OBJ_DIR = os.path.join(PKG_DIR, "_build")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = [
-    "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
+    "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
     "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr",
 ]
 
@@ -47,14 +56,18 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found; it is needed to build libgdr.so")
 
 
-def command(extra=(), out=LIB_PATH) -> list:
+def compile_command(source, obj, extra=()) -> list:
     return [nvcc_path(), *ARCH_FLAGS, *NVCC_FLAGS, *extra, "-I", INCLUDE, "-I", CSRC,
-            "-o", out, *SOURCES]
+            "-c", "-o", obj, source]
 
 
-def source_hash(flags=()) -> str:
+def link_command(objs, out=LIB_PATH) -> list:
+    return [nvcc_path(), *ARCH_FLAGS, "-shared", "-o", out, *objs]
+
+
+def source_hash(flags=(), files=None) -> str:
     h = hashlib.sha256()
-    for path in DEPS:
+    for path in DEPS if files is None else files:
         with open(path, "rb") as f:
             h.update(os.path.basename(path).encode())
             h.update(f.read())
@@ -62,10 +75,7 @@ def source_hash(flags=()) -> str:
     return h.hexdigest()
 
 
-def build(verbose: bool = False, extra=(), test_hooks: bool = False) -> str:
-    out = TEST_HOOKS_LIB_PATH if test_hooks else LIB_PATH
-    flags = TEST_HOOKS_FLAGS if test_hooks else []
-    cmd = command([*flags, *extra], out)
+def _run(cmd, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -73,6 +83,31 @@ def build(verbose: bool = False, extra=(), test_hooks: bool = False) -> str:
         raise RuntimeError(f"nvcc failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
     if verbose and (res.stdout or res.stderr):
         print(res.stdout + res.stderr, flush=True)
+
+
+def build(verbose: bool = False, extra=(), test_hooks: bool = False, reuse: bool = False) -> str:
+    """Compile every source, side by side, and link the library. With ``reuse``
+    an object whose sources and flags are unchanged is not compiled again."""
+    out = TEST_HOOKS_LIB_PATH if test_hooks else LIB_PATH
+    flags = TEST_HOOKS_FLAGS if test_hooks else []
+    os.makedirs(OBJ_DIR, exist_ok=True)
+
+    def one(source):
+        name = os.path.splitext(os.path.basename(source))[0]
+        obj = os.path.join(OBJ_DIR, name + ("_testhooks" if test_hooks else "") + ".o")
+        key = source_hash([*flags, *extra], UNITS[source])
+        if reuse and os.path.exists(obj) and os.path.exists(obj + ".srchash"):
+            with open(obj + ".srchash") as f:
+                if f.read().strip() == key:
+                    return obj
+        _run(compile_command(source, obj, [*flags, *extra]), verbose)
+        with open(obj + ".srchash", "w") as f:
+            f.write(key + "\n")
+        return obj
+
+    with concurrent.futures.ThreadPoolExecutor(len(UNITS)) as pool:
+        objs = list(pool.map(one, UNITS))
+    _run(link_command(objs, out), verbose)
     with open(out + ".srchash", "w") as f:
         f.write(source_hash(flags) + "\n")
     return out
@@ -88,7 +123,7 @@ def is_current(test_hooks: bool = False) -> bool:
 
 def ensure_built(verbose: bool = False, test_hooks: bool = False) -> str:
     if not is_current(test_hooks):
-        build(verbose=verbose, test_hooks=test_hooks)
+        build(verbose=verbose, test_hooks=test_hooks, reuse=True)
     return TEST_HOOKS_LIB_PATH if test_hooks else LIB_PATH
 
 

@@ -1,6 +1,7 @@
 // C ABI of libgdr (declared in include/gdr.h): host-side argument checks and
 // kernel dispatch for the recurrent gated-delta-rule decode step and the
-// standalone LinearAttentionGate op.
+// standalone LinearAttentionGate op. gdr_linear_api.cu holds the entry points
+// of linear attention with one decay per head and of the state cache.
 //
 // Everything here runs on the host before any launch. A failed check returns
 // its status with nothing queued; device values (lengths, slot indices) are
@@ -23,6 +24,7 @@
 #include "gdr_decode_rows.cuh"
 #include "gdr_decode_tma.cuh"
 #include "gdr_gate.cuh"
+#include "gdr_host.h"
 #include "gdr_prefill_tc.cuh"
 
 namespace {
@@ -730,6 +732,28 @@ int check_common_pointers(const gdr_bf16* query, const gdr_bf16* key, const gdr_
 
 }  // namespace
 
+// The helpers above for the library's other translation unit.
+namespace gdr_host {
+
+int fail(int status, const std::string& what) { return ::fail(status, what); }
+void set_last_launch(const gdr_launch_info& info) { g_last_launch = info; }
+bool aligned16(const void* ptr) { return ::aligned16(ptr); }
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return ::tensor_map_encoder(); }
+
+int current_device(Device* out) {
+  const cudaError_t err = cudaGetDevice(&out->ordinal);
+  if (err != cudaSuccess)
+    return fail(GDR_ERR_CUDA, std::string("cudaGetDevice: ") + cudaGetErrorString(err));
+  DeviceProps props;
+  const int rc = device_props(out->ordinal, &props);
+  if (rc != GDR_OK) return rc;
+  out->sms = props.sms;
+  out->smem_optin = props.smem_optin;
+  return GDR_OK;
+}
+
+}  // namespace gdr_host
+
 extern "C" {
 
 GDR_API int gdr_decode(const gdr_dims* dims, const gdr_bf16* query, const gdr_bf16* key,
@@ -875,9 +899,11 @@ GDR_API int gdr_device_error(uint32_t* flags, int reset) {
     const unsigned int zero = 0;
     err = cudaMemcpyToSymbol(gdr::g_device_error, &zero, sizeof(zero));
   }
+  unsigned int linear = 0;
+  if (err == cudaSuccess) err = gdr_host::linear_device_error(&linear, reset != 0);
   if (err != cudaSuccess)
     return fail(GDR_ERR_CUDA, std::string("reading the device error word: ") + cudaGetErrorString(err));
-  *flags = v;
+  *flags = v | linear;
   return GDR_OK;
 }
 
@@ -910,6 +936,7 @@ GDR_API int gdrtest_set_hooks(long long wait_limit_cycles, int hold_tile) {
   cudaError_t err = cudaMemcpyToSymbol(gdr::g_test_wait_limit, &limit, sizeof(limit));
   if (err == cudaSuccess)
     err = cudaMemcpyToSymbol(gdr::g_test_hold_tile, &hold_tile, sizeof(hold_tile));
+  if (err == cudaSuccess) err = gdr_host::linear_set_hooks(limit, hold_tile);
   if (err != cudaSuccess)
     return fail(GDR_ERR_CUDA, std::string("setting the test hooks: ") + cudaGetErrorString(err));
   return GDR_OK;

@@ -249,6 +249,96 @@ GDR_API int gdr_linear_attention_gate(const void* a, const void* b, const float*
                                       const float* decay_scale, void* decay, void* beta,
                                       int64_t rows, int32_t H, int dtype, gdr_stream_t stream);
 
+/*
+ * gdr_linear_attention_decode - linear attention with one decay per head, for
+ * one to eight tokens per item on the same state pool as gdr_decode. For every
+ * batch item b, value head h and token t < actual_seq_lengths[b], in order:
+ *   S = S * exp(log_decay[h]) + k (x) v
+ *   o = S^T (q * scale_value), stored as bfloat16
+ *
+ * Arguments, ownership, lengths, slots, committed counts, head grouping and
+ * alignment as for gdr_decode, with
+ *   log_decay   [H_v] fp32, usually <= 0; -infinity is a decay of 0 (the state
+ *               is the last token's outer product)
+ *   sizes       D_k in {64, 128}, D_v a positive multiple of 64, T in [1, 8],
+ *               dims->layout = GDR_LAYOUT_KV (GDR_LAYOUT_VK returns
+ *               GDR_ERR_UNSUPPORTED)
+ *   precision   fp32 throughout; the state is rounded to bf16 once per call.
+ * There are no beta, g and gk. Returns a gdr_status.
+ */
+GDR_API int gdr_linear_attention_decode(const gdr_dims* dims, const gdr_bf16* query,
+                                        const gdr_bf16* key, const gdr_bf16* value,
+                                        const float* log_decay, gdr_bf16* state_pool,
+                                        const int32_t* actual_seq_lengths,
+                                        const int32_t* ssm_state_indices,
+                                        const int32_t* num_accepted_tokens, float scale_value,
+                                        gdr_bf16* out, gdr_stream_t stream);
+
+/*
+ * gdr_linear_attention_prefill - the recurrence of gdr_linear_attention_decode
+ * over prompts of any length T >= 1, in chunks of 128 tokens on the tensor
+ * cores. Arguments as there, without num_accepted_tokens (all valid tokens are
+ * committed).
+ *   precision   fp32 sums; the state is carried in fp32 across the whole
+ *               prompt and rounded to bf16 once. Inside a chunk the weighted
+ *               products of queries and keys, the weighted keys, and the copy of the
+ *               chunk's first state that the queries read, are rounded to bf16.
+ *   infinities  an infinity or NaN among an item's valid tokens may reach the
+ *               outputs of the tokens before it in its chunk of 128. Padding
+ *               (t >= length) may hold anything.
+ * Tensor memory: as for gdr_prefill, a launch takes all 512 columns of each SM
+ * it runs on. Returns a gdr_status.
+ */
+GDR_API int gdr_linear_attention_prefill(const gdr_dims* dims, const gdr_bf16* query,
+                                         const gdr_bf16* key, const gdr_bf16* value,
+                                         const float* log_decay, gdr_bf16* state_pool,
+                                         const int32_t* actual_seq_lengths,
+                                         const int32_t* ssm_state_indices, float scale_value,
+                                         gdr_bf16* out, gdr_stream_t stream);
+
+/* Code types of the state cache. */
+typedef enum gdr_cache_type {
+  GDR_CACHE_INT8 = 0, /* two's complement, codes -127 .. 127 */
+  GDR_CACHE_E4M3 = 1  /* 8-bit float: 4 exponent and 3 mantissa bits, no infinities, |x| <= 448 */
+} gdr_cache_type;
+
+/*
+ * gdr_state_quantize - slots of a state pool written to an 8-bit cache: for
+ * i < n, slot ssm_state_indices[i] into entry cache_indices[i]. Every 64
+ * consecutive values of a slot share one fp32 scale; with m the largest
+ * magnitude of a group and top = 127 (int8) or 448 (e4m3),
+ *   scale = m / top,  code = round_to_nearest_even(x * (top / m))
+ * in fp32. A group with m < 2^-100 is held as zeros with scale 0; a group that
+ * holds an infinity or a NaN gets scale NaN and reads back as NaN.
+ *
+ *   state_pool         [pool_size, slot_values] bf16, read. Either pool layout:
+ *                      slot_values = H_v * D_k * D_v, a multiple of 64
+ *   ssm_state_indices  [n] int32
+ *   cache              [cache_size, slot_values] codes, written
+ *   scales             [cache_size, slot_values / 64] fp32, written
+ *   cache_indices      [n] int32, distinct (two pairs writing one entry race)
+ *   cache_type         a gdr_cache_type
+ * A pair whose slot or entry lies outside its range is skipped. Entries no
+ * pair names keep their bits. n = 0 queues nothing. state_pool, cache and
+ * scales must be 16-byte aligned. Returns a gdr_status.
+ */
+GDR_API int gdr_state_quantize(const gdr_bf16* state_pool, int32_t pool_size,
+                               const int32_t* ssm_state_indices, void* cache, float* scales,
+                               int32_t cache_size, const int32_t* cache_indices, int32_t n,
+                               int64_t slot_values, int cache_type, gdr_stream_t stream);
+
+/*
+ * gdr_state_dequantize - the reverse: for i < n, entry cache_indices[i] into
+ * slot ssm_state_indices[i] as bf16(code * scale). The slots must be distinct;
+ * one entry may go to several slots. A pair whose slot or entry lies outside
+ * its range is skipped; slots no pair names keep their bits. Everything else
+ * as for gdr_state_quantize. Returns a gdr_status.
+ */
+GDR_API int gdr_state_dequantize(const void* cache, const float* scales, int32_t cache_size,
+                                 const int32_t* cache_indices, gdr_bf16* state_pool,
+                                 int32_t pool_size, const int32_t* ssm_state_indices, int32_t n,
+                                 int64_t slot_values, int cache_type, gdr_stream_t stream);
+
 /* Static English name of a gdr_status value ("GDR_OK", ...); "unknown status"
  * for other values. Never NULL. */
 GDR_API const char* gdr_status_string(int status);
@@ -278,7 +368,10 @@ typedef enum gdr_kernel {
   GDR_KERNEL_TENSOR_CORE_ONE = 4,  /* the same kernel's form for one token per call */
   GDR_KERNEL_GATE = 5,             /* the standalone gate */
   GDR_KERNEL_PREFILL = 6,          /* gdr_prefill / gdr_prefill_gated */
-  GDR_KERNEL_ROWS = 7              /* one token on a k-contiguous pool, one row per lane group */
+  GDR_KERNEL_ROWS = 7,             /* one token on a k-contiguous pool, one row per lane group */
+  GDR_KERNEL_LINEAR_DECODE = 8,    /* gdr_linear_attention_decode */
+  GDR_KERNEL_LINEAR_PREFILL = 9,   /* gdr_linear_attention_prefill */
+  GDR_KERNEL_STATE_CACHE = 10      /* gdr_state_quantize / gdr_state_dequantize */
 } gdr_kernel;
 
 /* One kernel launch: its family, the key width, the column width of a tile
@@ -304,7 +397,7 @@ typedef struct gdr_launch_info {
  * Returns GDR_ERR_NULL for a NULL `info`, else GDR_OK. */
 GDR_API int gdr_last_launch(gdr_launch_info* info);
 
-/* The decode kernel forms the dispatcher can choose, as (kernel, D_k,
+/* The gated-delta-rule kernel forms the dispatcher can choose, as (kernel, D_k,
  * tile_cols, gated, layout); the launch-shape fields are 0. gdr_kernel_form
  * fills form `i`, 0 <= i < gdr_kernel_form_count(), and returns GDR_ERR_DIMS
  * for any other i. Host-only, needs no GPU; no counterpart on the pages. */
@@ -313,7 +406,9 @@ GDR_API int gdr_kernel_form(int i, gdr_launch_info* info);
 
 /* Library ABI version, currently 6 (2 added gdr_linear_attention_gate, 3 the
  * layout field of gdr_dims, 4 gdr_last_launch and the kernel forms, 5
- * gdr_prefill and gdr_prefill_gated, 6 the GDR_KERNEL_ROWS form). */
+ * gdr_prefill and gdr_prefill_gated, 6 the GDR_KERNEL_ROWS form). Entry points
+ * added since, gdr_linear_attention_decode and _prefill, gdr_state_quantize and
+ * _dequantize, change nothing that version 6 has and keep its number. */
 GDR_API int gdr_abi_version(void);
 
 #ifdef __cplusplus
