@@ -105,8 +105,11 @@ def lib() -> ctypes.CDLL:
         D, I = ctypes.POINTER(Dims), ctypes.c_int32
         L.gdr_linear_attention_decode.argtypes = [D, P, P, P, P, P, P, P, P, ctypes.c_float, P, P]
         L.gdr_linear_attention_decode.restype = ctypes.c_int
-        L.gdr_linear_attention_prefill.argtypes = [D, P, P, P, P, P, P, P, ctypes.c_float, P, P]
+        L.gdr_linear_attention_prefill.argtypes = [D, P, P, P, P, P, P, P, ctypes.c_float, P, P,
+                                                   ctypes.c_int64, P]
         L.gdr_linear_attention_prefill.restype = ctypes.c_int
+        L.gdr_linear_attention_prefill_workspace.argtypes = [D, ctypes.POINTER(ctypes.c_int64)]
+        L.gdr_linear_attention_prefill_workspace.restype = ctypes.c_int
         L.gdr_state_quantize.argtypes = [P, I, P, P, P, I, P, I, ctypes.c_int64, ctypes.c_int, P]
         L.gdr_state_quantize.restype = ctypes.c_int
         L.gdr_state_dequantize.argtypes = [P, P, I, P, P, I, P, I, ctypes.c_int64, ctypes.c_int,
@@ -457,10 +460,17 @@ def linear_attention_prefill(query: torch.Tensor, key: torch.Tensor, value: torc
                                      actual_seq_lengths, ssm_state_indices, None, out)
     with torch.cuda.device(device):
         stream = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+        need = ctypes.c_int64(0)
+        _check(lib().gdr_linear_attention_prefill_workspace(ctypes.byref(dims),
+                                                            ctypes.byref(need)))
+        # a workspace of this call's own: the allocator gives it to no other
+        # stream or graph while the call runs
+        work = None if need.value == 0 else torch.empty(need.value, dtype=torch.uint8,
+                                                        device=device)
         rc = lib().gdr_linear_attention_prefill(
             ctypes.byref(dims), _ptr(query), _ptr(key), _ptr(value), _ptr(log_decay),
             _ptr(state_pool), _ptr(actual_seq_lengths), _ptr(ssm_state_indices),
-            float(scale_value), _ptr(out), stream)
+            float(scale_value), _ptr(out), _ptr(work), need.value, stream)
     _check(rc)
     return out, state_pool
 

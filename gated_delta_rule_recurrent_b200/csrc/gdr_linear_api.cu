@@ -150,35 +150,73 @@ int encode_rows_map(const gdr_bf16* base, int D, int T, long long groups, CUtens
   return GDR_OK;
 }
 
-template <int DK>
-int launch_linear_prefill(const gdr::LinearParams& p, const gdr_host::Device& dev,
-                          cudaStream_t stream) {
-  using Shape = gdr::LpShape<DK>;
-  if (Shape::kSmem > dev.smem_optin)
+// How a call's chunks are cut: `segments` per tile of `seg_chunks` chunks.
+struct Segments {
+  int slices = 1, segments = 1, seg_chunks = 1;
+  int64_t workspace = 0;  // bytes
+};
+Segments plan_segments(const gdr_dims* d, int sms) {
+  Segments s;
+  s.slices = (d->D_v + gdr::kLpCols - 1) / gdr::kLpCols;
+  const int chunks = (d->T - 1) / gdr::kLpChunk + 1;
+  s.seg_chunks = chunks;
+  const long long tiles = static_cast<long long>(d->B) * d->H_v * s.slices;
+  if (3 * tiles > sms || chunks < 12) return s;
+  int n = static_cast<int>(sms / tiles);
+  if (n > chunks / 4) n = chunks / 4;
+  s.seg_chunks = (chunks - 1) / n + 1;
+  s.segments = (chunks - 1) / s.seg_chunks + 1;
+  s.workspace = tiles * s.segments * d->D_k * gdr::kLpCols * 4;
+  return s;
+}
+
+template <typename K>
+int opt_in_smem(K kernel, int smem, const gdr_host::Device& dev, std::atomic<bool>* ready) {
+  if (smem > dev.smem_optin)
     return fail(GDR_ERR_UNSUPPORTED, "prefill tile does not fit in shared memory");
+  if (ready[dev.ordinal].load(std::memory_order_acquire)) return GDR_OK;
+  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (err == cudaSuccess)
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
+  if (err != cudaSuccess)
+    return fail(GDR_ERR_CUDA, std::string("kernel attributes: ") + cudaGetErrorString(err));
+  ready[dev.ordinal].store(true, std::memory_order_release);
+  return GDR_OK;
+}
+
+template <int DK>
+int launch_linear_prefill(const gdr::LinearParams& p, const Segments& cut, float* workspace,
+                          const gdr_host::Device& dev, cudaStream_t stream) {
+  using Shape = gdr::LpShape<DK>;
+  using SegShape = gdr::LsShape<DK>;
+  static std::atomic<bool> ready[kMaxDevices], seg_ready[kMaxDevices];
   auto kernel = gdr::linear_prefill_kernel<DK>;
-  static std::atomic<bool> ready[kMaxDevices];
-  if (!ready[dev.ordinal].load(std::memory_order_acquire)) {
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           Shape::kSmem);
-    if (err == cudaSuccess)
-      err = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                 cudaSharedmemCarveoutMaxShared);
-    if (err != cudaSuccess)
-      return fail(GDR_ERR_CUDA, std::string("kernel attributes: ") + cudaGetErrorString(err));
-    ready[dev.ordinal].store(true, std::memory_order_release);
-  }
+  auto seg_kernel = gdr::linear_segment_kernel<DK>;
+  int rc = opt_in_smem(kernel, Shape::kSmem, dev, ready);
+  if (rc == GDR_OK) rc = opt_in_smem(seg_kernel, SegShape::kSmem, dev, seg_ready);
   CUtensorMap q_map, k_map, v_map, o_map;
-  const long long qk = static_cast<long long>(p.B) * p.H_qk, vo = static_cast<long long>(p.B) * p.H_v;
-  int rc = encode_rows_map(p.query, DK, p.T, qk, &q_map);
+  const long long qk = static_cast<long long>(p.B) * p.H_qk;
+  const long long vo = static_cast<long long>(p.B) * p.H_v;
+  if (rc == GDR_OK) rc = encode_rows_map(p.query, DK, p.T, qk, &q_map);
   if (rc == GDR_OK) rc = encode_rows_map(p.key, DK, p.T, qk, &k_map);
   if (rc == GDR_OK) rc = encode_rows_map(p.value, p.D_v, p.T, vo, &v_map);
   if (rc == GDR_OK) rc = encode_rows_map(p.out, p.D_v, p.T, vo, &o_map);
   if (rc != GDR_OK) return rc;
   gdr::LinearPrefillParams prm{};
   prm.p = p;
-  prm.slices = (p.D_v + gdr::kLpCols - 1) / gdr::kLpCols;
-  const int grid = p.B * p.H_v * prm.slices;
+  prm.slices = cut.slices;
+  prm.segments = cut.segments;
+  prm.seg_chunks = cut.seg_chunks;
+  prm.starts = workspace;
+  const int tiles = p.B * p.H_v * cut.slices;
+  if (cut.segments > 1) {
+    seg_kernel<<<tiles * (cut.segments - 1), gdr::kLsThreads, SegShape::kSmem, stream>>>(
+        k_map, v_map, prm);
+    gdr::linear_scan_kernel<DK>
+        <<<tiles * (DK * gdr::kLpCols / gdr::kLscanThreads), gdr::kLscanThreads, 0, stream>>>(prm);
+  }
+  const int grid = tiles * cut.segments;
   kernel<<<grid, gdr::kLpThreads, Shape::kSmem, stream>>>(q_map, k_map, v_map, o_map, prm);
   return launched("linear prefill", GDR_KERNEL_LINEAR_PREFILL, DK, gdr::kLpCols, GDR_LAYOUT_KV,
                   grid, gdr::kLpThreads, Shape::kSmem, Shape::kStages);
@@ -271,12 +309,25 @@ GDR_API int gdr_linear_attention_decode(const gdr_dims* dims, const gdr_bf16* qu
                          : launch_linear_decode<128>(p, dev.sms, st);
 }
 
+GDR_API int gdr_linear_attention_prefill_workspace(const gdr_dims* dims, int64_t* bytes) {
+  if (bytes == nullptr) return fail(GDR_ERR_NULL, "bytes is NULL");
+  *bytes = 0;
+  int rc = check_linear_dims(dims, 0);
+  if (rc != GDR_OK || dims->B == 0) return rc;
+  gdr_host::Device dev;
+  rc = gdr_host::current_device(&dev);
+  if (rc != GDR_OK) return rc;
+  *bytes = plan_segments(dims, dev.sms).workspace;
+  return GDR_OK;
+}
+
 GDR_API int gdr_linear_attention_prefill(const gdr_dims* dims, const gdr_bf16* query,
                                          const gdr_bf16* key, const gdr_bf16* value,
                                          const float* log_decay, gdr_bf16* state_pool,
                                          const int32_t* actual_seq_lengths,
                                          const int32_t* ssm_state_indices, float scale_value,
-                                         gdr_bf16* out, gdr_stream_t stream) {
+                                         gdr_bf16* out, void* workspace, int64_t workspace_bytes,
+                                         gdr_stream_t stream) {
   gdr_host::set_last_launch(gdr_launch_info{});
   int rc = check_linear_dims(dims, 0);
   if (rc != GDR_OK) return rc;
@@ -284,15 +335,22 @@ GDR_API int gdr_linear_attention_prefill(const gdr_dims* dims, const gdr_bf16* q
   rc = check_linear_pointers(query, key, value, log_decay, state_pool, actual_seq_lengths,
                              ssm_state_indices, out);
   if (rc != GDR_OK) return rc;
+  if (!gdr_host::aligned16(workspace))
+    return fail(GDR_ERR_ALIGN, "workspace must be 16-byte aligned");
   gdr_host::Device dev;
   rc = gdr_host::current_device(&dev);
   if (rc != GDR_OK) return rc;
+  const Segments cut = plan_segments(dims, dev.sms);
+  if (cut.workspace > 0 && (workspace == nullptr || workspace_bytes < cut.workspace))
+    return fail(GDR_ERR_NULL, "workspace is smaller than gdr_linear_attention_prefill_workspace "
+                              "asks for");
   const gdr::LinearParams p =
       linear_params(dims, query, key, value, log_decay, state_pool, actual_seq_lengths,
                     ssm_state_indices, nullptr, scale_value, out);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return dims->D_k == 64 ? launch_linear_prefill<64>(p, dev, st)
-                         : launch_linear_prefill<128>(p, dev, st);
+  float* ws = static_cast<float*>(workspace);
+  return dims->D_k == 64 ? launch_linear_prefill<64>(p, cut, ws, dev, st)
+                         : launch_linear_prefill<128>(p, cut, ws, dev, st);
 }
 
 GDR_API int gdr_state_quantize(const gdr_bf16* state_pool, int32_t pool_size,

@@ -19,17 +19,25 @@
 //            itself;
 //   out      (S^T q) lambda^{i+1} + P V, scaled, to bf16 in the chunk's v stage
 //            (both products have read v by then), TMA store;
-//   state    k in place times lambda^{C-1-j}; then S out of TMEM to bf16 in
-//            shared memory for the next chunk's S^T q, and back scaled by
+//   state    k in place times lambda^{C-1-j}; then S out of TMEM to a pair of
+//            bf16 tiles (S_hi, and S_lo = S - S_hi, which takes the place of
+//            the chunk's k) for the next chunk's S^T q, and back scaled by
 //            lambda^C for the next chunk's sum.
 // The mma warp issues the next chunk's q k^T right behind this chunk's P V, so
 // the tensor pipe waits only where the chain through the state is longer.
 //
 // Roundings to bf16, next to the fp32 sums: P and the weighted k, since the
-// other operand of their products is bf16 and one MMA takes one type; and the
-// copy of S that S^T q reads. Each is at most 2^-8 of its term, with a
-// random sign, about what the bf16 output's own rounding adds. The state
-// itself stays fp32 from the first chunk to the last.
+// other operand of their products is bf16 and one MMA takes one type. Each is
+// at most 2^-8 of its term, with a random sign, about what the bf16 output's own
+// rounding adds; with one of them behind each output the error is 1.4 times
+// that of the output's rounding alone. The state stays fp32 from the first
+// chunk to the last, and S^T q reads 16 significant bits of it.
+//
+// Long prompts of few heads: with fewer tiles than a third of the SMs the
+// chunks of a tile are cut into segments of a CTA each. A first pass sums each
+// segment's sum_j lambda^{end-1-j} k_j v_j^T (half the operands, one product a
+// chunk, no chain), a small scan turns those into the segments' first states,
+// and the main kernel starts each segment from its own.
 //
 // Rows behind an item's last token: k is weighted 0 and v zeroed by a write
 // (not a product: padding may hold NaN), q only reaches rows that are written
@@ -57,7 +65,7 @@ constexpr int kLpThreads = 512;
 constexpr int kLpBox = kLpChunk * 128;     // bytes of 128 rows x 64 bf16
 constexpr int kLpTmemCols = 512;
 constexpr int kLpTmemP = 0, kLpTmemInter = 128, kLpTmemIntra = 256, kLpTmemState = 384;
-constexpr int kLpBars = 8;                 // besides three per stage
+constexpr int kLpBars = 8;                 // besides six per stage
 
 template <int DK>
 struct LpShape {
@@ -66,18 +74,75 @@ struct LpShape {
   static constexpr int kStageBytes = (2 * kBoxes + 2) * kLpBox;  // q, k, v
   static constexpr int kStateOff = kStages * kStageBytes;        // bf16 S^T, [128 j][DK]
   static constexpr int kBarOff = kStateOff + kBoxes * kLpBox;
-  static constexpr int kPowOff = kBarOff + 8 * (3 * kStages + kLpBars) + 16;
+  static constexpr int kPowOff = kBarOff + 8 * (6 * kStages + kLpBars) + 16;
   static constexpr int kSmem = 1024 + kPowOff + 4 * (kLpChunk + 1);
 };
 
 struct LinearPrefillParams {
   LinearParams p;
   int slices;      // ceil(D_v / 128)
+  int segments;    // of a tile (1: not cut)
+  int seg_chunks;  // chunks of a segment
+  float* starts;   // [tiles, segments, D_k, 128]: entry g >= 1 is the sum of segment g - 1
+                   // after the first pass, the first state of segment g after the scan
 };
 
 // Byte offset of 16-byte chunk c (8 bf16) of row r in a [128 rows][64 columns]
 // box with the 128-byte swizzle.
 __device__ __forceinline__ int lp_swz(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
+
+// Row r of a chunk's k times `weight`, in place; `keep` false writes zeros. The
+// weight is a pair of bf16, w = hi + lo, and k w = k hi + (k lo) one fused bf16
+// operation behind a small product: the rounding of k w itself, and 2^-17 of
+// it, at half the instructions of the way through fp32. With the swizzle, 8
+// lanes (8 rows) touch 8 different groups of banks.
+template <int kBoxes>
+__device__ __forceinline__ void lp_weight_row(uint8_t* k_s, int r, float weight, bool keep) {
+  const __nv_bfloat16 hi = __float2bfloat16_rn(weight);
+  const __nv_bfloat16 lo = __float2bfloat16_rn(weight - __bfloat162float(hi));
+  const __nv_bfloat162 hi2 = __halves2bfloat162(hi, hi), lo2 = __halves2bfloat162(lo, lo);
+  const uint32_t valid = keep ? 0xffffffffu : 0u;
+#pragma unroll
+  for (int x = 0; x < kBoxes; ++x) {
+    uint4 w[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      w[c] = *reinterpret_cast<const uint4*>(k_s + x * kLpBox + lp_swz(r, c));
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      uint32_t y[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 k2 = *reinterpret_cast<const __nv_bfloat162*>(&y[e]);
+        const __nv_bfloat162 z = __hfma2(k2, hi2, __hmul2(k2, lo2));
+        y[e] = *reinterpret_cast<const uint32_t*>(&z) & valid;
+      }
+      *reinterpret_cast<uint4*>(k_s + x * kLpBox + lp_swz(r, c)) =
+          make_uint4(y[0], y[1], y[2], y[3]);
+    }
+  }
+}
+
+// 32 entries of row r of the transposed state (columns 32 j ..) as bf16 hi and
+// lo tiles.
+__device__ __forceinline__ void lp_store_state(uint8_t* hi_s, uint8_t* lo_s, int r, int j,
+                                               const uint32_t (&x)[32]) {
+  const unsigned long long neg1 = pk(-1.0f, -1.0f);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t y[4], z[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float a = __uint_as_float(x[8 * c + 2 * e]), b = __uint_as_float(x[8 * c + 2 * e + 1]);
+      y[e] = pack_bf16x2(a, b);
+      const float2 rem = upk(fma2(pk(bf16_lo(y[e]), bf16_hi(y[e])), neg1, pk(a, b)));
+      z[e] = pack_bf16x2(rem.x, rem.y);
+    }
+    const int off = (j >> 1) * kLpBox + lp_swz(r, 4 * (j & 1) + c);
+    *reinterpret_cast<uint4*>(hi_s + off) = make_uint4(y[0], y[1], y[2], y[3]);
+    *reinterpret_cast<uint4*>(lo_s + off) = make_uint4(z[0], z[1], z[2], z[3]);
+  }
+}
 
 template <int DK>
 __global__ void __launch_bounds__(kLpThreads, 1)
@@ -90,22 +155,33 @@ __global__ void __launch_bounds__(kLpThreads, 1)
   constexpr int kBoxes = Shape::kBoxes, kStages = Shape::kStages;
   const LinearParams& p = prm.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int slice = blockIdx.x % prm.slices;
-  const int bh = blockIdx.x / prm.slices;
+  const int seg = blockIdx.x % prm.segments;
+  const int tile = blockIdx.x / prm.segments;
+  const int slice = tile % prm.slices;
+  const int bh = tile / prm.slices;
   const int h = bh % p.H_v, b = bh / p.H_v;
   const int col0 = slice * kLpCols;
   const int cols = p.D_v - col0 < kLpCols ? p.D_v - col0 : kLpCols;  // 64 or 128
   int s, L, n;
   linear_item(p, b, s, L, n);
   uint16_t* out = p.out + static_cast<size_t>(bh) * p.T * p.D_v + col0;
-  const int n_chunks = (L + kLpChunk - 1) / kLpChunk;
-  if (L == 0) {  // empty or skipped: +0.0, the slot untouched
+  const int c0 = seg * prm.seg_chunks;  // this CTA's first chunk
+  const int all_chunks = (L + kLpChunk - 1) / kLpChunk;
+  const int own = all_chunks - c0 < prm.seg_chunks ? all_chunks - c0 : prm.seg_chunks;
+  if (own <= 0) {
+    // nothing but padding here: +0.0 (an empty or skipped item's slot is untouched)
     const int per_row = cols / 8;
-    for (int64_t e = tid; e < static_cast<int64_t>(p.T) * per_row; e += kLpThreads)
+    const int64_t first = static_cast<int64_t>(c0) * kLpChunk;
+    int64_t end = first + static_cast<int64_t>(prm.seg_chunks) * kLpChunk;
+    if (end > p.T) end = p.T;
+    for (int64_t e = first * per_row + tid; e < end * per_row; e += kLpThreads)
       *reinterpret_cast<uint4*>(out + (e / per_row) * p.D_v + (e % per_row) * 8) =
           make_uint4(0u, 0u, 0u, 0u);
     return;
   }
+  const int n_chunks = own;
+  const bool final_segment = c0 + own == all_chunks;
+  L -= c0 * kLpChunk;  // tokens from here on
 
   extern __shared__ __align__(16) uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
@@ -113,22 +189,21 @@ __global__ void __launch_bounds__(kLpThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Shape::kBarOff);
   float* pw = reinterpret_cast<float*>(smem + Shape::kPowOff);  // lambda^0 .. lambda^128
   const uint32_t bar0 = smem_addr(bars);
-  const uint32_t full = bar0;                      // + 8 st: q, k, v landed
-  const uint32_t qk_free = bar0 + 8 * kStages;     // + 8 st: q and k read for the last time
-  const uint32_t v_free = bar0 + 16 * kStages;     // + 8 st: the output has left the v stage
-  const uint32_t bar1 = bar0 + 24 * kStages;
+  const uint32_t q_full = bar0;                    // + 8 st: q landed
+  const uint32_t k_full = bar0 + 8 * kStages;      // + 8 st: k landed
+  const uint32_t v_full = bar0 + 16 * kStages;     // + 8 st: v landed
+  const uint32_t q_free = bar0 + 24 * kStages;     // + 8 st: q read for the last time
+  const uint32_t k_free = bar0 + 32 * kStages;     // + 8 st: k and the S_lo in its place read
+  const uint32_t v_free = bar0 + 40 * kStages;     // + 8 st: the output has left the v stage
+  const uint32_t bar1 = bar0 + 48 * kStages;
   const uint32_t p_raw = bar1, p_ready = bar1 + 8, k_ready = bar1 + 16, s_ready = bar1 + 24,
                  s_raw = bar1 + 32, o_raw = bar1 + 40, o_free = bar1 + 48, drained = bar1 + 56;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * kStages + kLpBars);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 6 * kStages + kLpBars);
   volatile int* abort_word = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const float log_decay = p.log_decay[h];
   if (tid == 0) {
-    for (int st = 0; st < kStages; ++st) {
-      mbar_init(full + 8 * st, 1);
-      mbar_init(qk_free + 8 * st, 1);
-      mbar_init(v_free + 8 * st, 1);
-    }
+    for (int x = 0; x < 6 * kStages; ++x) mbar_init(bar0 + 8 * x, 1);
     mbar_init(p_raw, 1);
     mbar_init(p_ready, 128);
     mbar_init(k_ready, 128);
@@ -155,33 +230,43 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     // ------------------------------------------------------------ load
     if (lane == 0 && !test_hold_tile(static_cast<int>(blockIdx.x))) {
       const int zq = b * p.H_qk + h / p.group;
-      const uint32_t bytes = (2 * kBoxes + cols / 64) * kLpBox;
-      int issued = 0;
+      int q_issued = 0, k_issued = 0, v_issued = 0;
       for (int i = 0; i < n_chunks; ++i) {
         const int st = i % kStages;
-        const uint32_t free_phase = ((i / kStages) & 1) ^ 1;
-        if (!mbar_wait_abandonable(qk_free + 8 * st, free_phase, abort_word, kErrProducerWait) ||
-            !mbar_wait_abandonable(v_free + 8 * st, free_phase, abort_word, kErrProducerWait))
-          break;
+        const uint32_t use = (i / kStages) & 1;
+        const int y = (c0 + i) * kLpChunk;
+        // S_lo of chunk j sits in the k stage of chunk j - 1, that of chunk 0 in
+        // the last stage: that stage is freed once before its first load
+        const uint32_t k_phase = st == kStages - 1 ? use : use ^ 1;
         const uint32_t dst = smem_addr(smem + st * Shape::kStageBytes);
-        mbar_expect_tx(full + 8 * st, bytes);
+        if (!mbar_wait_abandonable(q_free + 8 * st, use ^ 1, abort_word, kErrProducerWait)) break;
+        mbar_expect_tx(q_full + 8 * st, kBoxes * kLpBox);
 #pragma unroll
-        for (int x = 0; x < kBoxes; ++x) {
-          tma_load_3d(dst + x * kLpBox, &q_map, 64 * x, i * kLpChunk, zq, full + 8 * st);
-          tma_load_3d(dst + (kBoxes + x) * kLpBox, &k_map, 64 * x, i * kLpChunk, zq,
-                      full + 8 * st);
-        }
+        for (int x = 0; x < kBoxes; ++x)
+          tma_load_3d(dst + x * kLpBox, &q_map, 64 * x, y, zq, q_full + 8 * st);
+        mbar_arrive(q_full + 8 * st);
+        ++q_issued;
+        if (!mbar_wait_abandonable(k_free + 8 * st, k_phase, abort_word, kErrProducerWait)) break;
+        mbar_expect_tx(k_full + 8 * st, kBoxes * kLpBox);
+#pragma unroll
+        for (int x = 0; x < kBoxes; ++x)
+          tma_load_3d(dst + (kBoxes + x) * kLpBox, &k_map, 64 * x, y, zq, k_full + 8 * st);
+        mbar_arrive(k_full + 8 * st);
+        ++k_issued;
+        if (!mbar_wait_abandonable(v_free + 8 * st, use ^ 1, abort_word, kErrProducerWait)) break;
+        mbar_expect_tx(v_full + 8 * st, cols / 64 * kLpBox);
         for (int x = 0; x < cols / 64; ++x)
-          tma_load_3d(dst + (2 * kBoxes + x) * kLpBox, &v_map, col0 + 64 * x, i * kLpChunk, bh,
-                      full + 8 * st);
-        mbar_arrive(full + 8 * st);
-        ++issued;
+          tma_load_3d(dst + (2 * kBoxes + x) * kLpBox, &v_map, col0 + 64 * x, y, bh,
+                      v_full + 8 * st);
+        mbar_arrive(v_full + 8 * st);
+        ++v_issued;
       }
-      for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-        if (!mbar_wait_bounded(full + 8 * (i % kStages), (i / kStages) & 1)) {
-          flag_error(kErrDrainWait);
-          break;
-        }
+      // no copy may outlive the CTA: the last load of every stage has landed
+      const int issued[3] = {q_issued, k_issued, v_issued};
+      for (int x = 0; x < 3; ++x)
+        for (int i = issued[x] > kStages ? issued[x] - kStages : 0; i < issued[x]; ++i)
+          if (!mbar_wait_bounded(q_full + 8 * (x * kStages + i % kStages), (i / kStages) & 1))
+            flag_error(kErrDrainWait);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ mma
@@ -205,7 +290,8 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         const uint64_t k_k = umma_desc(k_s, 16, 1024, kUmmaSwizzle128);
         const uint64_t k_mn = umma_desc(k_s, kLpBox, 1024, kUmmaSwizzle128);
         const uint64_t v_mn = umma_desc(v_s, kLpBox, 1024, kUmmaSwizzle128);
-        if (!wait(full + 8 * st, (i / kStages) & 1)) break;
+        const uint32_t use = (i / kStages) & 1;
+        if (!wait(q_full + 8 * st, use) || !wait(k_full + 8 * st, use)) break;
 #pragma unroll
         for (int ks = 0; ks < DK / 16; ++ks) {
           const uint32_t off = (ks >> 2) * kLpBox + (ks & 3) * 32;
@@ -215,13 +301,25 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         umma_commit(p_raw);
         if (!wait(s_ready, ph)) break;
         if (i > 0 && !wait(o_free, ph ^ 1)) break;
+        const int lo_st = (i + kStages - 1) % kStages;  // the k stage that holds S_lo
+        const uint64_t lo_desc =
+            umma_desc(smem_addr(smem + lo_st * Shape::kStageBytes + kBoxes * kLpBox), 16, 1024,
+                      kUmmaSwizzle128);
 #pragma unroll
         for (int ks = 0; ks < DK / 16; ++ks) {
           const uint32_t off = (ks >> 2) * kLpBox + (ks & 3) * 32;
           umma_bf16(tmem + kLpTmemInter, umma_desc_advance(q_k, off),
                     umma_desc_advance(s_desc, off), id_qk, ks > 0);
         }
-        if (!wait(k_ready, ph)) break;
+#pragma unroll
+        for (int ks = 0; ks < DK / 16; ++ks) {
+          const uint32_t off = (ks >> 2) * kLpBox + (ks & 3) * 32;
+          umma_bf16(tmem + kLpTmemInter, umma_desc_advance(q_k, off),
+                    umma_desc_advance(lo_desc, off), id_qk, true);
+        }
+        umma_commit(q_free + 8 * st);
+        umma_commit(k_free + 8 * lo_st);
+        if (!wait(v_full + 8 * st, use) || !wait(k_ready, ph)) break;
 #pragma unroll
         for (int ks = 0; ks < kLpChunk / 16; ++ks)
           umma_bf16(tmem + kLpTmemState, umma_desc_advance(v_mn, ks * 2048),
@@ -233,24 +331,27 @@ __global__ void __launch_bounds__(kLpThreads, 1)
           umma_bf16_ts(tmem + kLpTmemIntra, tmem + kLpTmemP + 8 * ks,
                        umma_desc_advance(v_mn, ks * 2048), id_pv, ks > 0);
         umma_commit(o_raw);
-        umma_commit(qk_free + 8 * st);
       }
       umma_commit(drained);
       if (!mbar_wait_bounded(drained, 0)) flag_error(kErrDrainWait);
     }
   } else if (warp < 4) {
     // ------------------------------------------------------------ padding
-    // tokens behind the last chunk: +0.0
+    // this CTA's tokens behind the last chunk: +0.0
     const int per_row = cols / 8;
-    const int64_t end = static_cast<int64_t>(p.T) * per_row;
-    for (int64_t e = static_cast<int64_t>(n_chunks) * kLpChunk * per_row + (tid - 64); e < end;
-         e += 64)
+    int64_t end = static_cast<int64_t>(c0 + prm.seg_chunks) * kLpChunk;
+    end = (end < p.T ? end : p.T) * per_row;
+    for (int64_t e = static_cast<int64_t>(c0 + n_chunks) * kLpChunk * per_row + (tid - 64);
+         e < end; e += 64)
       *reinterpret_cast<uint4*>(out + (e / per_row) * p.D_v + (e % per_row) * 8) =
           make_uint4(0u, 0u, 0u, 0u);
   } else if (warp < 8) {
     // ------------------------------------------------------------ P
     const int wq = warp & 3, t = tid & 127;
     const uint32_t base = tmem + kLpTmemP + (static_cast<uint32_t>(32 * wq) << 16);
+    unsigned long long w2[16];  // lambda^{31-e}
+#pragma unroll
+    for (int e = 0; e < 16; ++e) w2[e] = pk(pw[31 - 2 * e], pw[30 - 2 * e]);
     for (int i = 0; i < n_chunks; ++i) {
       const bool ok = mbar_wait_abandonable(p_raw, i & 1, abort_word, kErrConsumerWait);
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -258,17 +359,29 @@ __global__ void __launch_bounds__(kLpThreads, 1)
 #pragma unroll 1
       for (int j = 0; j < 4; ++j) {
         uint32_t y[16];
-        if (j <= wq) {  // columns 32 j .. of rows 32 wq ..: some are unmasked
+        if (j <= wq) {
           uint32_t x[32];
           tmem_ld32(base + 32 * j, x);
           tmem_wait_ld();
-          const float* pt = pw + (t - 32 * j);
+          if (j < wq) {
+            // all 32 columns are behind row t: lambda^{t-c} as
+            // lambda^{t-32j-31} lambda^{31-e}, two packed products a pair
+            const float a = pw[t - 32 * j - 31];
+            const unsigned long long a2 = pk(a, a);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int c = 32 * j + 2 * e;
-            const float a = c <= t ? __uint_as_float(x[2 * e]) * pt[-2 * e] : 0.0f;
-            const float d = c + 1 <= t ? __uint_as_float(x[2 * e + 1]) * pt[-2 * e - 1] : 0.0f;
-            y[e] = pack_bf16x2(a, d);
+            for (int e = 0; e < 16; ++e) {
+              const float2 f = upk(mul2(mul2(pk(__uint_as_float(x[2 * e]),
+                                                __uint_as_float(x[2 * e + 1])), a2), w2[e]));
+              y[e] = pack_bf16x2(f.x, f.y);
+            }
+          } else {
+            // the diagonal block: what is ahead of row t is set to 0
+            const float* pt = pw + lane;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              y[e] = pack_bf16x2(
+                  2 * e <= lane ? __uint_as_float(x[2 * e]) * pt[-2 * e] : 0.0f,
+                  2 * e + 1 <= lane ? __uint_as_float(x[2 * e + 1]) * pt[-2 * e - 1] : 0.0f);
           }
         } else {
 #pragma unroll
@@ -285,10 +398,11 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     const int wq = warp & 3, t = tid & 127;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * wq) << 16);
     const float inter = pw[t + 1] * p.scale;
+    const unsigned long long inter2 = pk(inter, inter), scale2 = pk(p.scale, p.scale);
     const bool elected = t == 0;
     for (int i = 0; i < n_chunks; ++i) {
       const int st = i % kStages;
-      const int Lc = L - i * kLpChunk;
+      const uint32_t valid = t < L - i * kLpChunk ? 0xffffffffu : 0u;  // padding: +0.0
       uint8_t* o_s = smem + st * Shape::kStageBytes + 2 * kBoxes * kLpBox;
       const bool ok =
           __all_sync(0xffffffffu, mbar_wait_abandonable(o_raw, i & 1, abort_word,
@@ -307,11 +421,10 @@ __global__ void __launch_bounds__(kLpThreads, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int k = 8 * c + 2 * e;
-              y[e] = t < Lc ? pack_bf16x2(fmaf(__uint_as_float(x[k]), inter,
-                                               __uint_as_float(z[k]) * p.scale),
-                                          fmaf(__uint_as_float(x[k + 1]), inter,
-                                               __uint_as_float(z[k + 1]) * p.scale))
-                            : 0u;
+              const float2 f = upk(
+                  fma2(pk(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), inter2,
+                       mul2(pk(__uint_as_float(z[k]), __uint_as_float(z[k + 1])), scale2)));
+              y[e] = pack_bf16x2(f.x, f.y) & valid;
             }
             *reinterpret_cast<uint4*>(o_s + (j >> 1) * kLpBox + lp_swz(t, 4 * (j & 1) + c)) =
                 make_uint4(y[0], y[1], y[2], y[3]);
@@ -324,7 +437,8 @@ __global__ void __launch_bounds__(kLpThreads, 1)
       if (!named_barrier_and(1, 128, ok)) break;
       if (elected) {
         for (int x = 0; x < cols / 64; ++x)
-          tma_store_3d(&o_map, col0 + 64 * x, i * kLpChunk, bh, smem_addr(o_s + x * kLpBox));
+          tma_store_3d(&o_map, col0 + 64 * x, (c0 + i) * kLpChunk, bh,
+                       smem_addr(o_s + x * kLpBox));
         bulk_commit_group();
         bulk_wait_read_all();
         mbar_arrive(v_free + 8 * st);
@@ -339,23 +453,28 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     const bool live = r < cols;
     uint16_t* slot =
         p.state_pool + (static_cast<size_t>(s) * p.H_v + h) * DK * p.D_v + col0 + r;
-    // the slot: bf16 as it is for the first S^T q, scaled into TMEM for the first sum
+    // the first state: as hi and lo for the first S^T q, scaled into TMEM for
+    // the first sum
     {
       const float decay = pw[L < kLpChunk ? L : kLpChunk];
+      const float* start = prm.starts + static_cast<size_t>(blockIdx.x) * DK * kLpCols + r;
+      uint8_t* lo_s = smem + (kStages - 1) * Shape::kStageBytes + kBoxes * kLpBox;
 #pragma unroll 1
       for (int j = 0; j < DK / 32; ++j) {
         uint32_t x[32];
+        if (seg > 0) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          x[e] = live ? slot[static_cast<size_t>(32 * j + e) * p.D_v] : 0u;
+          for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(start[(32 * j + e) * kLpCols]);
+        } else {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          *reinterpret_cast<uint4*>(s_s + (j >> 1) * kLpBox + lp_swz(r, 4 * (j & 1) + c)) =
-              make_uint4(x[8 * c] | (x[8 * c + 1] << 16), x[8 * c + 2] | (x[8 * c + 3] << 16),
-                         x[8 * c + 4] | (x[8 * c + 5] << 16),
-                         x[8 * c + 6] | (x[8 * c + 7] << 16));
+          for (int e = 0; e < 32; ++e)
+            x[e] = live ? static_cast<uint32_t>(slot[static_cast<size_t>(32 * j + e) * p.D_v])
+                              << 16
+                        : 0u;
+        }
+        lp_store_state(s_s, lo_s, r, j, x);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e] << 16) * decay);
+        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * decay);
         tmem_st32(lanes + 32 * j, x);
       }
       tmem_wait_st();
@@ -365,34 +484,25 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     }
     for (int i = 0; i < n_chunks; ++i) {
       const int st = i % kStages;
+      const uint32_t use = (i / kStages) & 1;
       const int left = L - i * kLpChunk;
       const int Lc = left < kLpChunk ? left : kLpChunk;
       uint8_t* k_s = smem + st * Shape::kStageBytes + kBoxes * kLpBox;
       uint8_t* v_s = k_s + kBoxes * kLpBox;
-      bool ok = mbar_wait_abandonable(full + 8 * st, (i / kStages) & 1, abort_word,
-                                      kErrConsumerWait) &&
+      // q k^T has read k (and waited for it to land)
+      bool ok = mbar_wait_abandonable(k_full + 8 * st, use, abort_word, kErrConsumerWait) &&
                 mbar_wait_abandonable(p_raw, i & 1, abort_word, kErrConsumerWait);
       if (!__all_sync(0xffffffffu, ok)) break;
-      // row r of k times lambda^{Lc-1-r}. Lanes start at different 16-byte
-      // pieces of their rows, so that 8 lanes of a row group hit 8 bank groups.
-      const float weight = r < Lc ? pw[Lc - 1 - r] : 0.0f;
+      lp_weight_row<kBoxes>(k_s, r, r < Lc ? pw[Lc - 1 - r] : 0.0f, r < Lc);
+      if (Lc < kLpChunk) {  // rows of v behind the last token: zeros
+        ok = mbar_wait_abandonable(v_full + 8 * st, use, abort_word, kErrConsumerWait);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (r >= Lc) {
 #pragma unroll
-      for (int x = 0; x < kBoxes; ++x)
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint4* at = reinterpret_cast<uint4*>(k_s + x * kLpBox + lp_swz(r, c));
-          uint4 w = *at;
-          uint32_t y[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            y[e] = r < Lc ? pack_bf16x2(bf16_lo(y[e]) * weight, bf16_hi(y[e]) * weight) : 0u;
-          *at = make_uint4(y[0], y[1], y[2], y[3]);
+          for (int c = 0; c < 16; ++c)
+            *reinterpret_cast<uint4*>(v_s + (c >> 3) * kLpBox + lp_swz(r, c & 7)) =
+                make_uint4(0u, 0u, 0u, 0u);
         }
-      if (r >= Lc) {
-#pragma unroll
-        for (int c = 0; c < 16; ++c)
-          *reinterpret_cast<uint4*>(v_s + (c >> 3) * kLpBox + lp_swz(r, c & 7)) =
-              make_uint4(0u, 0u, 0u, 0u);
       }
       fence_async_smem();
       mbar_arrive(k_ready);
@@ -408,7 +518,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         tmem_ld32(lanes + 32 * j, x);
         tmem_wait_ld();
         if (last) {
-          if (live) {
+          if (live && final_segment) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               slot[static_cast<size_t>(32 * j + e) * p.D_v] =
@@ -416,16 +526,8 @@ __global__ void __launch_bounds__(kLpThreads, 1)
           }
           continue;
         }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t y[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            y[e] = pack_bf16x2(__uint_as_float(x[8 * c + 2 * e]),
-                               __uint_as_float(x[8 * c + 2 * e + 1]));
-          *reinterpret_cast<uint4*>(s_s + (j >> 1) * kLpBox + lp_swz(r, 4 * (j & 1) + c)) =
-              make_uint4(y[0], y[1], y[2], y[3]);
-        }
+        // the sum has read this chunk's k: its stage takes S_lo
+        lp_store_state(s_s, k_s, r, j, x);
 #pragma unroll
         for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * decay);
         tmem_st32(lanes + 32 * j, x);
@@ -446,6 +548,201 @@ __global__ void __launch_bounds__(kLpThreads, 1)
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, kLpTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- segments
+
+// First pass: the sum of a segment that another one follows, which is
+// prm.seg_chunks whole chunks:  sum_j lambda^{end-1-j} k_j v_j^T  over its
+// tokens j, into the next segment's entry of prm.starts as [D_k][128 columns]
+// fp32. The weights reach from the segment's end, so the chunks' products add
+// up in TMEM and nothing waits for the state. 64 KB a chunk at D_k = 128: HBM
+// bounds it once the segments fill the SMs.
+template <int DK>
+struct LsShape {
+  static constexpr int kBoxes = DK / 64;
+  static constexpr int kStages = 3;
+  static constexpr int kStageBytes = (kBoxes + 2) * kLpBox;  // k, v
+  static constexpr int kBarOff = kStages * kStageBytes;
+  static constexpr int kSmem = 1024 + kBarOff + 8 * (3 * kStages + 2) + 16;
+};
+constexpr int kLsThreads = 192;  // load, mma, and four warps that weight k and store
+
+template <int DK>
+__global__ void __launch_bounds__(kLsThreads, 1)
+    linear_segment_kernel(const __grid_constant__ CUtensorMap k_map,
+                          const __grid_constant__ CUtensorMap v_map,
+                          const LinearPrefillParams prm) {
+  using Shape = LsShape<DK>;
+  constexpr int kBoxes = Shape::kBoxes, kStages = Shape::kStages;
+  const LinearParams& p = prm.p;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int seg = blockIdx.x % (prm.segments - 1);
+  const int tile = blockIdx.x / (prm.segments - 1);
+  const int slice = tile % prm.slices;
+  const int bh = tile / prm.slices;
+  const int h = bh % p.H_v, b = bh / p.H_v;
+  const int col0 = slice * kLpCols;
+  const int cols = p.D_v - col0 < kLpCols ? p.D_v - col0 : kLpCols;
+  int s, L, n;
+  linear_item(p, b, s, L, n);
+  const int64_t end = static_cast<int64_t>(seg + 1) * prm.seg_chunks * kLpChunk;
+  if (L <= end) return;  // the item's last segment, or behind it
+  const int c0 = seg * prm.seg_chunks;
+  const int n_chunks = prm.seg_chunks;
+
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Shape::kBarOff);
+  const uint32_t full = smem_addr(bars);          // + 8 st: k and v landed
+  const uint32_t ready = full + 8 * kStages;      // + 8 st: k weighted
+  const uint32_t free_ = full + 16 * kStages;     // + 8 st: the product has read them
+  const uint32_t summed = full + 24 * kStages, drained = summed + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * kStages + 2);
+  volatile int* abort_word = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  if (tid == 0) {
+    for (int st = 0; st < kStages; ++st) {
+      mbar_init(full + 8 * st, 1);
+      mbar_init(ready + 8 * st, 128);
+      mbar_init(free_ + 8 * st, 1);
+    }
+    mbar_init(summed, 1);
+    mbar_init(drained, 1);
+    *abort_word = 0;
+    fence_mbar_init();
+  }
+  __syncwarp();
+  if (warp == 4) {
+    tmem_alloc(smem_addr(tmem_slot), 128);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 4) {
+    // ------------------------------------------------------------ load
+    if (lane == 0) {
+      const int zk = b * p.H_qk + h / p.group;
+      int issued = 0;
+      for (int i = 0; i < n_chunks; ++i) {
+        const int st = i % kStages;
+        const int y = (c0 + i) * kLpChunk;
+        const uint32_t dst = smem_addr(smem + st * Shape::kStageBytes);
+        if (!mbar_wait_abandonable(free_ + 8 * st, ((i / kStages) & 1) ^ 1, abort_word,
+                                   kErrProducerWait))
+          break;
+        mbar_expect_tx(full + 8 * st, (kBoxes + cols / 64) * kLpBox);
+#pragma unroll
+        for (int x = 0; x < kBoxes; ++x)
+          tma_load_3d(dst + x * kLpBox, &k_map, 64 * x, y, zk, full + 8 * st);
+        for (int x = 0; x < cols / 64; ++x)
+          tma_load_3d(dst + (kBoxes + x) * kLpBox, &v_map, col0 + 64 * x, y, bh, full + 8 * st);
+        mbar_arrive(full + 8 * st);
+        ++issued;
+      }
+      for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+        if (!mbar_wait_bounded(full + 8 * (i % kStages), (i / kStages) & 1))
+          flag_error(kErrDrainWait);
+    }
+  } else if (warp == 5) {
+    // ------------------------------------------------------------ mma
+    if (lane == 0) {
+      constexpr uint32_t id_kv = umma_idesc_bf16<128, DK, true, true>();
+      bool ok = true;
+      for (int i = 0; i < n_chunks && ok; ++i) {
+        const int st = i % kStages;
+        const uint32_t k_s = smem_addr(smem + st * Shape::kStageBytes);
+        const uint64_t k_mn = umma_desc(k_s, kLpBox, 1024, kUmmaSwizzle128);
+        const uint64_t v_mn = umma_desc(k_s + kBoxes * kLpBox, kLpBox, 1024, kUmmaSwizzle128);
+        ok = mbar_wait_abandonable(full + 8 * st, (i / kStages) & 1, abort_word,
+                                   kErrConsumerWait) &&
+             mbar_wait_abandonable(ready + 8 * st, (i / kStages) & 1, abort_word,
+                                   kErrConsumerWait);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < kLpChunk / 16; ++ks)
+          umma_bf16(tmem, umma_desc_advance(v_mn, ks * 2048), umma_desc_advance(k_mn, ks * 2048),
+                    id_kv, i > 0 || ks > 0);
+        umma_commit(free_ + 8 * st);
+      }
+      if (ok) umma_commit(summed);
+      umma_commit(drained);
+      if (!mbar_wait_bounded(drained, 0)) flag_error(kErrDrainWait);
+    }
+  } else {
+    // ------------------------------------------------------------ weights, store
+    const float log_decay = p.log_decay[h];
+    const int r = tid;
+    bool ok = true;
+    for (int i = 0; i < n_chunks; ++i) {
+      const int st = i % kStages;
+      const float weight = decay_power(log_decay, (n_chunks - i) * kLpChunk - 1 - r);
+      ok = mbar_wait_abandonable(full + 8 * st, (i / kStages) & 1, abort_word, kErrConsumerWait);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      lp_weight_row<kBoxes>(smem + st * Shape::kStageBytes, r, weight, true);
+      fence_async_smem();
+      mbar_arrive(ready + 8 * st);
+    }
+    ok = ok && mbar_wait_abandonable(summed, 0, abort_word, kErrConsumerWait);
+    if (__all_sync(0xffffffffu, ok)) {
+      tc_fence_after();
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+      float* dst = prm.starts +
+                   (static_cast<size_t>(tile) * prm.segments + seg + 1) * DK * kLpCols + r;
+#pragma unroll 1
+      for (int j = 0; j < DK / 32; ++j) {
+        uint32_t x[32];
+        tmem_ld32(lanes + 32 * j, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) dst[(32 * j + e) * kLpCols] = __uint_as_float(x[e]);
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 128);
+  }
+}
+
+// The scan: entry g of prm.starts from the sum of segment g - 1 to the first
+// state of segment g,  start_g = lambda^{segment} start_{g-1} + sum_{g-1}, with
+// start_0 the slot. A thread takes one state value of one tile.
+constexpr int kLscanThreads = 256;
+template <int DK>
+__global__ void __launch_bounds__(kLscanThreads) linear_scan_kernel(const LinearPrefillParams prm) {
+  constexpr int kBlocks = DK * kLpCols / kLscanThreads;  // of a tile
+  const LinearParams& p = prm.p;
+  const int tile = blockIdx.x / kBlocks;
+  const int e = (blockIdx.x % kBlocks) * kLscanThreads + threadIdx.x;
+  const int row = e / kLpCols, col = (tile % prm.slices) * kLpCols + e % kLpCols;
+  const int bh = tile / prm.slices;
+  const int h = bh % p.H_v, b = bh / p.H_v;
+  int s, L, n;
+  linear_item(p, b, s, L, n);
+  const int tokens = prm.seg_chunks * kLpChunk;
+  const int count = (L + tokens - 1) / tokens;  // segments of this item
+  if (count <= 1) return;
+  const float decay = decay_power(p.log_decay[h], tokens);
+  float* at = prm.starts + static_cast<size_t>(tile) * prm.segments * DK * kLpCols + e;
+  float x = 0.0f;
+  if (col < p.D_v)
+    x = bf16_bits_to_f32(
+        p.state_pool[((static_cast<size_t>(s) * p.H_v + h) * DK + row) * p.D_v + col]);
+#pragma unroll 4
+  for (int g = 1; g < count; ++g) {
+    float* here = at + static_cast<size_t>(g) * DK * kLpCols;
+    x = fmaf(decay, x, *here);
+    *here = x;
   }
 }
 

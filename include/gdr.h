@@ -281,11 +281,17 @@ GDR_API int gdr_linear_attention_decode(const gdr_dims* dims, const gdr_bf16* qu
  * committed).
  *   precision   fp32 sums; the state is carried in fp32 across the whole
  *               prompt and rounded to bf16 once. Inside a chunk the weighted
- *               products of queries and keys, the weighted keys, and the copy of the
- *               chunk's first state that the queries read, are rounded to bf16.
+ *               products of queries and keys and the weighted keys are rounded
+ *               to bf16; the queries read 16 significant bits of the state.
  *   infinities  an infinity or NaN among an item's valid tokens may reach the
  *               outputs of the tokens before it in its chunk of 128. Padding
  *               (t >= length) may hold anything.
+ *   workspace   device memory of at least the bytes that
+ *               gdr_linear_attention_prefill_workspace gives for `dims` (0 for
+ *               most calls; NULL is fine then), 16-byte aligned, for this call
+ *               alone until its work is done: two calls that may run at the
+ *               same time, or two captured graphs that may, need one each.
+ *               A smaller one returns GDR_ERR_NULL.
  * Tensor memory: as for gdr_prefill, a launch takes all 512 columns of each SM
  * it runs on. Returns a gdr_status.
  */
@@ -294,7 +300,14 @@ GDR_API int gdr_linear_attention_prefill(const gdr_dims* dims, const gdr_bf16* q
                                          const float* log_decay, gdr_bf16* state_pool,
                                          const int32_t* actual_seq_lengths,
                                          const int32_t* ssm_state_indices, float scale_value,
-                                         gdr_bf16* out, gdr_stream_t stream);
+                                         gdr_bf16* out, void* workspace, int64_t workspace_bytes,
+                                         gdr_stream_t stream);
+
+/* Bytes of workspace a call of gdr_linear_attention_prefill with these sizes
+ * needs on the current device: more than 0 when there are few heads and items
+ * for the device's SMs and the prompt is long (its chunks are then cut into
+ * segments that run side by side). Host-only. Returns a gdr_status. */
+GDR_API int gdr_linear_attention_prefill_workspace(const gdr_dims* dims, int64_t* bytes);
 
 /* Code types of the state cache. */
 typedef enum gdr_cache_type {
@@ -407,8 +420,8 @@ GDR_API int gdr_kernel_form(int i, gdr_launch_info* info);
 /* Library ABI version, currently 6 (2 added gdr_linear_attention_gate, 3 the
  * layout field of gdr_dims, 4 gdr_last_launch and the kernel forms, 5
  * gdr_prefill and gdr_prefill_gated, 6 the GDR_KERNEL_ROWS form). Entry points
- * added since, gdr_linear_attention_decode and _prefill, gdr_state_quantize and
- * _dequantize, change nothing that version 6 has and keep its number. */
+ * added since, gdr_linear_attention_decode, _prefill and _prefill_workspace,
+ * gdr_state_quantize and _dequantize, change nothing that version 6 has and keep its number. */
 GDR_API int gdr_abi_version(void);
 
 #ifdef __cplusplus

@@ -166,7 +166,7 @@ def _c_call(dims, op="decode", ptr=16, nulls=()):
     d = None if dims is None else ctypes.byref(binding.Dims(*dims))
     if op == "decode":
         return L.gdr_linear_attention_decode(d, *a[:7], None, ctypes.c_float(1.0), a[7], None)
-    return L.gdr_linear_attention_prefill(d, *a[:7], ctypes.c_float(1.0), a[7], None)
+    return L.gdr_linear_attention_prefill(d, *a[:7], ctypes.c_float(1.0), a[7], None, 0, None)
 
 
 @NO_DEVICE
@@ -291,6 +291,11 @@ PREFILL = [
     (2, 1, 1, 640, 128, 128, 2),
     (2, 1, 1, 900, 64, 64, 2),
     (1, 1, 1, 1300, 128, 64, 1),
+    # few tiles and 12 chunks or more: cut into segments
+    (1, 1, 1, 1536, 64, 128, 2),
+    (2, 1, 2, 1700, 128, 192, 3),
+    (3, 1, 1, 2900, 64, 320, 3),
+    (1, 1, 1, 5000, 128, 64, 1),
 ]
 
 
