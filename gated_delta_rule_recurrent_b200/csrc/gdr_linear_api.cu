@@ -57,6 +57,8 @@ int check_linear_dims(const gdr_dims* d, int max_T) {
   const long long bh = static_cast<long long>(d->B) * d->H_v;
   if (bh > kMaxGrid || bh * (d->D_v / 64) > kMaxGrid)
     return fail(GDR_ERR_DIMS, "B * H_v * D_v / 64 exceeds 2^31 - 1");
+  if (static_cast<long long>(d->pool_size) * d->H_v > kMaxGrid)
+    return fail(GDR_ERR_DIMS, "pool_size * H_v exceeds 2^31 - 1");
   // row strides of a TMA map stay below 2^40 bytes
   const long long wide = d->D_v > d->D_k ? d->D_v : d->D_k;
   if (static_cast<long long>(d->T) * wide >= (1LL << 38))
@@ -132,15 +134,16 @@ int launch_linear_decode(const gdr::LinearParams& p, int sms, cudaStream_t strea
 
 // ---------------------------------------------------------------- prefill
 
-// [groups, T, D] bf16 as boxes of 64 columns x 128 rows of one group.
-int encode_rows_map(const gdr_bf16* base, int D, int T, long long groups, CUtensorMap* map) {
+// [groups, T, D] bf16 as boxes of 64 columns x `rows` rows of one group.
+int encode_rows_map(const gdr_bf16* base, int D, int T, long long groups, int rows,
+                    CUtensorMap* map) {
   PFN_cuTensorMapEncodeTiled_v12000 encode = gdr_host::tensor_map_encoder();
   if (encode == nullptr) return fail(GDR_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
   const cuuint64_t gdim[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(T),
                               static_cast<cuuint64_t>(groups)};
   const cuuint64_t gstride[2] = {static_cast<cuuint64_t>(D) * 2,
                                  static_cast<cuuint64_t>(T) * D * 2};
-  const cuuint32_t box[3] = {64, gdr::kLpChunk, 1};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(rows), 1};
   const cuuint32_t estride[3] = {1, 1, 1};
   const CUresult cr =
       encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<gdr_bf16*>(base), gdim, gstride,
@@ -185,6 +188,24 @@ int opt_in_smem(K kernel, int smem, const gdr_host::Device& dev, std::atomic<boo
   return GDR_OK;
 }
 
+// A launch that, with `overlap`, may start before the one ahead of it on the
+// stream is done (the kernel waits for that one where it needs its results).
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), int grid, int threads, int smem, bool overlap,
+                         cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = overlap ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int DK>
 int launch_linear_prefill(const gdr::LinearParams& p, const Segments& cut, float* workspace,
                           const gdr_host::Device& dev, cudaStream_t stream) {
@@ -195,13 +216,16 @@ int launch_linear_prefill(const gdr::LinearParams& p, const Segments& cut, float
   auto seg_kernel = gdr::linear_segment_kernel<DK>;
   int rc = opt_in_smem(kernel, Shape::kSmem, dev, ready);
   if (rc == GDR_OK) rc = opt_in_smem(seg_kernel, SegShape::kSmem, dev, seg_ready);
-  CUtensorMap q_map, k_map, v_map, o_map;
+  CUtensorMap q_map, k_map, v_map, o_map, pool_map;
   const long long qk = static_cast<long long>(p.B) * p.H_qk;
   const long long vo = static_cast<long long>(p.B) * p.H_v;
-  if (rc == GDR_OK) rc = encode_rows_map(p.query, DK, p.T, qk, &q_map);
-  if (rc == GDR_OK) rc = encode_rows_map(p.key, DK, p.T, qk, &k_map);
-  if (rc == GDR_OK) rc = encode_rows_map(p.value, p.D_v, p.T, vo, &v_map);
-  if (rc == GDR_OK) rc = encode_rows_map(p.out, p.D_v, p.T, vo, &o_map);
+  const long long slots = static_cast<long long>(p.pool_size) * p.H_v;
+  constexpr int rows = gdr::kLpChunk;
+  if (rc == GDR_OK) rc = encode_rows_map(p.query, DK, p.T, qk, rows, &q_map);
+  if (rc == GDR_OK) rc = encode_rows_map(p.key, DK, p.T, qk, rows, &k_map);
+  if (rc == GDR_OK) rc = encode_rows_map(p.value, p.D_v, p.T, vo, rows, &v_map);
+  if (rc == GDR_OK) rc = encode_rows_map(p.out, p.D_v, p.T, vo, rows, &o_map);
+  if (rc == GDR_OK) rc = encode_rows_map(p.state_pool, p.D_v, DK, slots, DK, &pool_map);
   if (rc != GDR_OK) return rc;
   gdr::LinearPrefillParams prm{};
   prm.p = p;
@@ -210,14 +234,22 @@ int launch_linear_prefill(const gdr::LinearParams& p, const Segments& cut, float
   prm.seg_chunks = cut.seg_chunks;
   prm.starts = workspace;
   const int tiles = p.B * p.H_v * cut.slices;
+  const int grid = tiles * cut.segments;
+  prm.by_length = cut.segments == 1 && tiles > dev.sms && p.B > 1 && p.B <= gdr::kLpSortItems;
+  cudaError_t err = cudaSuccess;
   if (cut.segments > 1) {
     seg_kernel<<<tiles * (cut.segments - 1), gdr::kLsThreads, SegShape::kSmem, stream>>>(
         k_map, v_map, prm);
-    gdr::linear_scan_kernel<DK>
-        <<<tiles * (DK * gdr::kLpCols / gdr::kLscanThreads), gdr::kLscanThreads, 0, stream>>>(prm);
+    err = cudaGetLastError();
+    if (err == cudaSuccess)
+      err = launch_after(gdr::linear_scan_kernel<DK>, tiles * (DK * gdr::kLpCols / gdr::kLscanThreads),
+                         gdr::kLscanThreads, 0, true, stream, prm);
   }
-  const int grid = tiles * cut.segments;
-  kernel<<<grid, gdr::kLpThreads, Shape::kSmem, stream>>>(q_map, k_map, v_map, o_map, prm);
+  if (err == cudaSuccess)
+    err = launch_after(kernel, grid, gdr::kLpThreads, Shape::kSmem, cut.segments > 1, stream, q_map,
+                       k_map, v_map, o_map, pool_map, prm);
+  if (err != cudaSuccess)
+    return fail(GDR_ERR_CUDA, std::string("linear prefill launch: ") + cudaGetErrorString(err));
   return launched("linear prefill", GDR_KERNEL_LINEAR_PREFILL, DK, gdr::kLpCols, GDR_LAYOUT_KV,
                   grid, gdr::kLpThreads, Shape::kSmem, Shape::kStages);
 }

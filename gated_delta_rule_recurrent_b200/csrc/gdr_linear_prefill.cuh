@@ -62,10 +62,12 @@ namespace gdr {
 constexpr int kLpChunk = 128;              // tokens of a chunk
 constexpr int kLpCols = 128;               // columns of D_v of a CTA
 constexpr int kLpThreads = 512;
+constexpr int kLpSortItems = 256;          // items whose lengths a CTA ranks, at most
+constexpr int kLpRegsFew = 40, kLpRegsMany = 152;  // 128 * 40 + 384 * 152 <= 65536
 constexpr int kLpBox = kLpChunk * 128;     // bytes of 128 rows x 64 bf16
 constexpr int kLpTmemCols = 512;
 constexpr int kLpTmemP = 0, kLpTmemInter = 128, kLpTmemIntra = 256, kLpTmemState = 384;
-constexpr int kLpBars = 8;                 // besides six per stage
+constexpr int kLpBars = 9;                 // besides six per stage
 
 template <int DK>
 struct LpShape {
@@ -83,13 +85,37 @@ struct LinearPrefillParams {
   int slices;      // ceil(D_v / 128)
   int segments;    // of a tile (1: not cut)
   int seg_chunks;  // chunks of a segment
-  float* starts;   // [tiles, segments, D_k, 128]: entry g >= 1 is the sum of segment g - 1
-                   // after the first pass, the first state of segment g after the scan
+  int by_length;   // nonzero: tiles in the order of their items' lengths, longest first
+  // [tiles, segments, D_k / 4, 128 columns, 4 rows]: entry g >= 1 is the sum of segment
+  // g - 1 after the first pass, the first state of segment g after the scan. Four rows
+  // of a column are one 16-byte access, coalesced over the columns.
+  float* starts;
 };
 
 // Byte offset of 16-byte chunk c (8 bf16) of row r in a [128 rows][64 columns]
 // box with the 128-byte swizzle.
-__device__ __forceinline__ int lp_swz(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
+__device__ __forceinline__ int lp_swz(int r, int c) {
+  return (r * 128 + ((r & 7) << 4)) ^ (c << 4);
+}
+
+// Move registers between warpgroups (every warp of the group executes it).
+template <int N>
+__device__ __forceinline__ void lp_regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void lp_regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Until the launch before this one is done and its writes are visible (no
+// effect on a launch that does not overlap with the one before).
+__device__ __forceinline__ void lp_grid_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void lp_grid_launch_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 
 // Row r of a chunk's k times `weight`, in place; `keep` false writes zeros. The
 // weight is a pair of bf16, w = hi + lo, and k w = k hi + (k lo) one fused bf16
@@ -144,19 +170,47 @@ __device__ __forceinline__ void lp_store_state(uint8_t* hi_s, uint8_t* lo_s, int
   }
 }
 
+// Byte offset of column j of row i in a slot's tile as the TMA lays it out:
+// [column / 64][D_k rows][64 columns], 128-byte swizzle.
+template <int DK>
+__device__ __forceinline__ int lp_tile_offset(int i, int j) {
+  return (j >> 6) * DK * 128 + lp_swz(i, (j & 63) >> 3) + (j & 7) * 2;
+}
+
 template <int DK>
 __global__ void __launch_bounds__(kLpThreads, 1)
     linear_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
                           const __grid_constant__ CUtensorMap k_map,
                           const __grid_constant__ CUtensorMap v_map,
                           const __grid_constant__ CUtensorMap o_map,
+                          const __grid_constant__ CUtensorMap pool_map,
                           const LinearPrefillParams prm) {
   using Shape = LpShape<DK>;
   constexpr int kBoxes = Shape::kBoxes, kStages = Shape::kStages;
   const LinearParams& p = prm.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int seg = blockIdx.x % prm.segments;
-  const int tile = blockIdx.x / prm.segments;
+  int tile = blockIdx.x / prm.segments;
+  if (prm.by_length) {
+    // more tiles than SMs: the SMs that are done first take the short ones. The
+    // item whose rank among the lengths is this tile's item number:
+    __shared__ int lengths[kLpSortItems], item;
+    int own_length = 0;
+    if (tid < p.B) {
+      int s_, n_;
+      linear_item(p, tid, s_, own_length, n_);
+      lengths[tid] = own_length;
+    }
+    __syncthreads();
+    if (tid < p.B) {
+      int rank = 0;
+      for (int j = 0; j < p.B; ++j)
+        rank += lengths[j] > own_length || (lengths[j] == own_length && j < tid);
+      if (rank == tile / (p.H_v * prm.slices)) item = tid;
+    }
+    __syncthreads();
+    tile = item * p.H_v * prm.slices + tile % (p.H_v * prm.slices);
+  }
   const int slice = tile % prm.slices;
   const int bh = tile / prm.slices;
   const int h = bh % p.H_v, b = bh / p.H_v;
@@ -171,6 +225,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
   if (own <= 0) {
     // nothing but padding here: +0.0 (an empty or skipped item's slot is untouched)
     const int per_row = cols / 8;
+    lp_grid_wait();
     const int64_t first = static_cast<int64_t>(c0) * kLpChunk;
     int64_t end = first + static_cast<int64_t>(prm.seg_chunks) * kLpChunk;
     if (end > p.T) end = p.T;
@@ -197,11 +252,28 @@ __global__ void __launch_bounds__(kLpThreads, 1)
   const uint32_t v_free = bar0 + 40 * kStages;     // + 8 st: the output has left the v stage
   const uint32_t bar1 = bar0 + 48 * kStages;
   const uint32_t p_raw = bar1, p_ready = bar1 + 8, k_ready = bar1 + 16, s_ready = bar1 + 24,
-                 s_raw = bar1 + 32, o_raw = bar1 + 40, o_free = bar1 + 48, drained = bar1 + 56;
+                 s_raw = bar1 + 32, o_raw = bar1 + 40, o_free = bar1 + 48, drained = bar1 + 56,
+                 slot_full = bar1 + 64;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 6 * kStages + kLpBars);
   volatile int* abort_word = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
+  // The loader, warp 0's first lane, starts on the first stages ahead of the
+  // set-up of the CTA (they wait for nobody); the rest follows below.
+  const int zq = b * p.H_qk + h / p.group;
+  int issued[3] = {0, 0, 0};  // loads of q, k and v
+  const auto load = [&](int kind, const CUtensorMap* map, int i, int x0, int z, int boxes) {
+    const int st = i % kStages;
+    const uint32_t bar = q_full + 8 * (kind * kStages + st);
+    const uint32_t dst =
+        smem_addr(smem + st * Shape::kStageBytes + kind * kBoxes * kLpBox);
+    mbar_expect_tx(bar, boxes * kLpBox);
+    for (int x = 0; x < boxes; ++x)
+      tma_load_3d(dst + x * kLpBox, map, x0 + 64 * x, (c0 + i) * kLpChunk, z, bar);
+    mbar_arrive(bar);
+    ++issued[kind];
+  };
   const float log_decay = p.log_decay[h];
+  const bool loads = tid == 0 && !test_hold_tile(static_cast<int>(blockIdx.x));
   if (tid == 0) {
     for (int x = 0; x < 6 * kStages; ++x) mbar_init(bar0 + 8 * x, 1);
     mbar_init(p_raw, 1);
@@ -212,12 +284,26 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     mbar_init(o_raw, 1);
     mbar_init(o_free, 128);
     mbar_init(drained, 1);
+    mbar_init(slot_full, 1);
     *abort_word = 0;
     fence_mbar_init();
+    fence_async_smem();
+    if (loads) {
+      load(0, &q_map, 0, 0, zq, kBoxes);
+      load(1, &k_map, 0, 0, zq, kBoxes);
+      if (seg == 0) {  // the slot, where S_hi will be
+        mbar_expect_tx(slot_full, cols / 64 * DK * 128);
+        for (int x = 0; x < cols / 64; ++x)
+          tma_load_3d(smem_addr(smem + Shape::kStateOff + x * DK * 128), &pool_map, col0 + 64 * x,
+                      0, s * p.H_v + h, slot_full);
+        mbar_arrive(slot_full);
+      }
+      load(2, &v_map, 0, col0, bh, cols / 64);
+    }
   }
   if (tid >= 128 && tid <= 128 + kLpChunk) pw[tid - 128] = decay_power(log_decay, tid - 128);
   __syncwarp();
-  if (warp == 0) {
+  if (warp == 1) {
     tmem_alloc(smem_addr(tmem_slot), kLpTmemCols);
     tmem_relinquish();
   }
@@ -226,47 +312,29 @@ __global__ void __launch_bounds__(kLpThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  if (warp < 4) lp_regs_dec<kLpRegsFew>();
   if (warp == 0) {
     // ------------------------------------------------------------ load
-    if (lane == 0 && !test_hold_tile(static_cast<int>(blockIdx.x))) {
-      const int zq = b * p.H_qk + h / p.group;
-      int q_issued = 0, k_issued = 0, v_issued = 0;
-      for (int i = 0; i < n_chunks; ++i) {
+    if (loads) {
+      for (int i = 1; i < n_chunks; ++i) {
         const int st = i % kStages;
         const uint32_t use = (i / kStages) & 1;
-        const int y = (c0 + i) * kLpChunk;
         // S_lo of chunk j sits in the k stage of chunk j - 1, that of chunk 0 in
         // the last stage: that stage is freed once before its first load
         const uint32_t k_phase = st == kStages - 1 ? use : use ^ 1;
-        const uint32_t dst = smem_addr(smem + st * Shape::kStageBytes);
         if (!mbar_wait_abandonable(q_free + 8 * st, use ^ 1, abort_word, kErrProducerWait)) break;
-        mbar_expect_tx(q_full + 8 * st, kBoxes * kLpBox);
-#pragma unroll
-        for (int x = 0; x < kBoxes; ++x)
-          tma_load_3d(dst + x * kLpBox, &q_map, 64 * x, y, zq, q_full + 8 * st);
-        mbar_arrive(q_full + 8 * st);
-        ++q_issued;
+        load(0, &q_map, i, 0, zq, kBoxes);
         if (!mbar_wait_abandonable(k_free + 8 * st, k_phase, abort_word, kErrProducerWait)) break;
-        mbar_expect_tx(k_full + 8 * st, kBoxes * kLpBox);
-#pragma unroll
-        for (int x = 0; x < kBoxes; ++x)
-          tma_load_3d(dst + (kBoxes + x) * kLpBox, &k_map, 64 * x, y, zq, k_full + 8 * st);
-        mbar_arrive(k_full + 8 * st);
-        ++k_issued;
+        load(1, &k_map, i, 0, zq, kBoxes);
         if (!mbar_wait_abandonable(v_free + 8 * st, use ^ 1, abort_word, kErrProducerWait)) break;
-        mbar_expect_tx(v_full + 8 * st, cols / 64 * kLpBox);
-        for (int x = 0; x < cols / 64; ++x)
-          tma_load_3d(dst + (2 * kBoxes + x) * kLpBox, &v_map, col0 + 64 * x, y, bh,
-                      v_full + 8 * st);
-        mbar_arrive(v_full + 8 * st);
-        ++v_issued;
+        load(2, &v_map, i, col0, bh, cols / 64);
       }
       // no copy may outlive the CTA: the last load of every stage has landed
-      const int issued[3] = {q_issued, k_issued, v_issued};
       for (int x = 0; x < 3; ++x)
         for (int i = issued[x] > kStages ? issued[x] - kStages : 0; i < issued[x]; ++i)
           if (!mbar_wait_bounded(q_full + 8 * (x * kStages + i % kStages), (i / kStages) & 1))
             flag_error(kErrDrainWait);
+      if (seg == 0 && !mbar_wait_bounded(slot_full, 0)) flag_error(kErrDrainWait);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ mma
@@ -277,10 +345,11 @@ __global__ void __launch_bounds__(kLpThreads, 1)
       const uint64_t s_desc =
           umma_desc(smem_addr(smem + Shape::kStateOff), 16, 1024, kUmmaSwizzle128);
       auto wait = [&](uint32_t bar, uint32_t phase) {
-        const bool ok = mbar_wait_abandonable(bar, phase, abort_word, kErrConsumerWait);
+        const bool done = mbar_wait_abandonable(bar, phase, abort_word, kErrConsumerWait);
         tc_fence_after();
-        return ok;
+        return done;
       };
+      bool ok = true;
       for (int i = 0; i < n_chunks; ++i) {
         const int st = i % kStages;
         const uint32_t ph = i & 1;
@@ -295,41 +364,58 @@ __global__ void __launch_bounds__(kLpThreads, 1)
 #pragma unroll
         for (int ks = 0; ks < DK / 16; ++ks) {
           const uint32_t off = (ks >> 2) * kLpBox + (ks & 3) * 32;
-          umma_bf16(tmem + kLpTmemP, umma_desc_advance(q_k, off), umma_desc_advance(k_k, off),
-                    id_qk, ks > 0);
+          umma_bf16_at(tmem + kLpTmemP, q_k, off, k_k, off, id_qk, ks > 0);
         }
         umma_commit(p_raw);
-        if (!wait(s_ready, ph)) break;
+        const bool from_slot = i == 0 && seg == 0;
+        if (!wait(from_slot ? slot_full : s_ready, ph)) break;
         if (i > 0 && !wait(o_free, ph ^ 1)) break;
         const int lo_st = (i + kStages - 1) % kStages;  // the k stage that holds S_lo
-        const uint64_t lo_desc =
-            umma_desc(smem_addr(smem + lo_st * Shape::kStageBytes + kBoxes * kLpBox), 16, 1024,
-                      kUmmaSwizzle128);
+        if (from_slot) {
+          // the slot's tile is S itself, rows of 64 columns: the other major-ness,
+          // and bf16 has no S_lo
+          const uint64_t tile_desc =
+              umma_desc(smem_addr(smem + Shape::kStateOff), DK * 128, 1024, kUmmaSwizzle128);
+#pragma unroll 1
+          for (int ks = 0; ks < DK / 16; ++ks)
+            umma_bf16_at(tmem + kLpTmemInter, q_k, (ks >> 2) * kLpBox + (ks & 3) * 32, tile_desc,
+                         ks * 2048, id_pv, ks > 0);
+        } else {
+          const uint64_t lo_desc =
+              umma_desc(smem_addr(smem + lo_st * Shape::kStageBytes + kBoxes * kLpBox), 16, 1024,
+                        kUmmaSwizzle128);
 #pragma unroll
-        for (int ks = 0; ks < DK / 16; ++ks) {
-          const uint32_t off = (ks >> 2) * kLpBox + (ks & 3) * 32;
-          umma_bf16(tmem + kLpTmemInter, umma_desc_advance(q_k, off),
-                    umma_desc_advance(s_desc, off), id_qk, ks > 0);
-        }
+          for (int ks = 0; ks < DK / 16; ++ks) {
+            const uint32_t off = (ks >> 2) * kLpBox + (ks & 3) * 32;
+            umma_bf16_at(tmem + kLpTmemInter, q_k, off, s_desc, off, id_qk, ks > 0);
+          }
 #pragma unroll
-        for (int ks = 0; ks < DK / 16; ++ks) {
-          const uint32_t off = (ks >> 2) * kLpBox + (ks & 3) * 32;
-          umma_bf16(tmem + kLpTmemInter, umma_desc_advance(q_k, off),
-                    umma_desc_advance(lo_desc, off), id_qk, true);
+          for (int ks = 0; ks < DK / 16; ++ks) {
+            const uint32_t off = (ks >> 2) * kLpBox + (ks & 3) * 32;
+            umma_bf16_at(tmem + kLpTmemInter, q_k, off, lo_desc, off, id_qk, true);
+          }
         }
         umma_commit(q_free + 8 * st);
         umma_commit(k_free + 8 * lo_st);
+        if (from_slot && !wait(s_ready, ph)) break;  // the scaled slot, in TMEM
         if (!wait(v_full + 8 * st, use) || !wait(k_ready, ph)) break;
 #pragma unroll
         for (int ks = 0; ks < kLpChunk / 16; ++ks)
-          umma_bf16(tmem + kLpTmemState, umma_desc_advance(v_mn, ks * 2048),
-                    umma_desc_advance(k_mn, ks * 2048), id_kv, true);
+          umma_bf16_at(tmem + kLpTmemState, v_mn, ks * 2048, k_mn, ks * 2048, id_kv, true);
         umma_commit(s_raw);
-        if (!wait(p_ready, ph)) break;
+        // The first time round the instructions of P V are run once with the MMA
+        // switched off, so that fetching them (3500 cycles, cold) falls into the wait.
+        for (int run = i > 0; run < 2; ++run) {
+          if (run && !wait(p_ready, ph)) {
+            ok = false;
+            break;
+          }
 #pragma unroll
-        for (int ks = 0; ks < kLpChunk / 16; ++ks)
-          umma_bf16_ts(tmem + kLpTmemIntra, tmem + kLpTmemP + 8 * ks,
-                       umma_desc_advance(v_mn, ks * 2048), id_pv, ks > 0);
+          for (int ks = 0; ks < kLpChunk / 16; ++ks)
+            umma_bf16_ts_at(tmem + kLpTmemIntra, tmem + kLpTmemP + 8 * ks, v_mn, ks * 2048, id_pv,
+                            ks > 0, run != 0);
+        }
+        if (!ok) break;
         umma_commit(o_raw);
       }
       umma_commit(drained);
@@ -338,6 +424,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
   } else if (warp < 4) {
     // ------------------------------------------------------------ padding
     // this CTA's tokens behind the last chunk: +0.0
+    lp_grid_wait();
     const int per_row = cols / 8;
     int64_t end = static_cast<int64_t>(c0 + prm.seg_chunks) * kLpChunk;
     end = (end < p.T ? end : p.T) * per_row;
@@ -347,6 +434,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
           make_uint4(0u, 0u, 0u, 0u);
   } else if (warp < 8) {
     // ------------------------------------------------------------ P
+    lp_regs_inc<kLpRegsMany>();
     const int wq = warp & 3, t = tid & 127;
     const uint32_t base = tmem + kLpTmemP + (static_cast<uint32_t>(32 * wq) << 16);
     unsigned long long w2[16];  // lambda^{31-e}
@@ -395,6 +483,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------ out
+    lp_regs_inc<kLpRegsMany>();
     const int wq = warp & 3, t = tid & 127;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * wq) << 16);
     const float inter = pw[t + 1] * p.scale;
@@ -447,32 +536,41 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     if (elected) bulk_wait_all();
   } else {
     // ------------------------------------------------------------ state
+    lp_regs_inc<kLpRegsMany>();
     const int wq = warp & 3, r = tid & 127;  // r: column j of S, row of k and v
     const uint32_t lanes = tmem + kLpTmemState + (static_cast<uint32_t>(32 * wq) << 16);
     uint8_t* s_s = smem + Shape::kStateOff;
-    const bool live = r < cols;
-    uint16_t* slot =
-        p.state_pool + (static_cast<size_t>(s) * p.H_v + h) * DK * p.D_v + col0 + r;
-    // the first state: as hi and lo for the first S^T q, scaled into TMEM for
-    // the first sum
+    const bool elected = r == 0;
+    bool ok = true;
+    // the first state, scaled, into TMEM for the first sum; a segment's as hi and
+    // lo for its first S^T q too (the slot's tile serves that as it is)
     {
       const float decay = pw[L < kLpChunk ? L : kLpChunk];
-      const float* start = prm.starts + static_cast<size_t>(blockIdx.x) * DK * kLpCols + r;
+      const float* start = prm.starts + static_cast<size_t>(blockIdx.x) * DK * kLpCols + 4 * r;
       uint8_t* lo_s = smem + (kStages - 1) * Shape::kStageBytes + kBoxes * kLpBox;
+      if (seg == 0)
+        ok = __all_sync(0xffffffffu, mbar_wait_abandonable(slot_full, 0, abort_word,
+                                                           kErrConsumerWait));
 #pragma unroll 1
       for (int j = 0; j < DK / 32; ++j) {
         uint32_t x[32];
         if (seg > 0) {
+          if (j == 0) lp_grid_wait();  // the scan's results
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(start[(32 * j + e) * kLpCols]);
+          for (int e = 0; e < 8; ++e) {
+            const float4 f = *reinterpret_cast<const float4*>(start + (8 * j + e) * 4 * kLpCols);
+            x[4 * e] = __float_as_uint(f.x);
+            x[4 * e + 1] = __float_as_uint(f.y);
+            x[4 * e + 2] = __float_as_uint(f.z);
+            x[4 * e + 3] = __float_as_uint(f.w);
+          }
+          lp_store_state(s_s, lo_s, r, j, x);
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            x[e] = live ? static_cast<uint32_t>(slot[static_cast<size_t>(32 * j + e) * p.D_v])
-                              << 16
-                        : 0u;
+            x[e] = static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(
+                       s_s + lp_tile_offset<DK>(32 * j + e, r))) << 16;
         }
-        lp_store_state(s_s, lo_s, r, j, x);
 #pragma unroll
         for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * decay);
         tmem_st32(lanes + 32 * j, x);
@@ -480,7 +578,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
       tmem_wait_st();
       fence_async_smem();
       tc_fence_before();
-      mbar_arrive(s_ready);
+      if (ok) mbar_arrive(s_ready);
     }
     for (int i = 0; i < n_chunks; ++i) {
       const int st = i % kStages;
@@ -490,13 +588,15 @@ __global__ void __launch_bounds__(kLpThreads, 1)
       uint8_t* k_s = smem + st * Shape::kStageBytes + kBoxes * kLpBox;
       uint8_t* v_s = k_s + kBoxes * kLpBox;
       // q k^T has read k (and waited for it to land)
-      bool ok = mbar_wait_abandonable(k_full + 8 * st, use, abort_word, kErrConsumerWait) &&
-                mbar_wait_abandonable(p_raw, i & 1, abort_word, kErrConsumerWait);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      ok = ok && mbar_wait_abandonable(k_full + 8 * st, use, abort_word, kErrConsumerWait) &&
+           mbar_wait_abandonable(p_raw, i & 1, abort_word, kErrConsumerWait);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
       lp_weight_row<kBoxes>(k_s, r, r < Lc ? pw[Lc - 1 - r] : 0.0f, r < Lc);
       if (Lc < kLpChunk) {  // rows of v behind the last token: zeros
-        ok = mbar_wait_abandonable(v_full + 8 * st, use, abort_word, kErrConsumerWait);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        ok = __all_sync(0xffffffffu, mbar_wait_abandonable(v_full + 8 * st, use, abort_word,
+                                                           kErrConsumerWait));
+        if (!ok) break;
         if (r >= Lc) {
 #pragma unroll
           for (int c = 0; c < 16; ++c)
@@ -507,36 +607,55 @@ __global__ void __launch_bounds__(kLpThreads, 1)
       fence_async_smem();
       mbar_arrive(k_ready);
 
-      ok = mbar_wait_abandonable(s_raw, i & 1, abort_word, kErrConsumerWait);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      // the sum is done and has read this chunk's k: its stage takes S_lo
+      ok = __all_sync(0xffffffffu,
+                      mbar_wait_abandonable(s_raw, i & 1, abort_word, kErrConsumerWait));
+      if (!ok) break;
       tc_fence_after();
-      const bool last = i + 1 == n_chunks;
+      if (i + 1 == n_chunks) break;
       const float decay = pw[left - Lc < kLpChunk ? left - Lc : kLpChunk];
+      const unsigned long long decay2 = pk(decay, decay);
 #pragma unroll 1
       for (int j = 0; j < DK / 32; ++j) {
         uint32_t x[32];
         tmem_ld32(lanes + 32 * j, x);
         tmem_wait_ld();
-        if (last) {
-          if (live && final_segment) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              slot[static_cast<size_t>(32 * j + e) * p.D_v] =
-                  f32_to_bf16_bits(__uint_as_float(x[e]));
-          }
-          continue;
-        }
-        // the sum has read this chunk's k: its stage takes S_lo
         lp_store_state(s_s, k_s, r, j, x);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * decay);
+        for (int e = 0; e < 32; e += 2) {
+          const float2 f =
+              upk(mul2(decay2, pk(__uint_as_float(x[e]), __uint_as_float(x[e + 1]))));
+          x[e] = __float_as_uint(f.x);
+          x[e + 1] = __float_as_uint(f.y);
+        }
         tmem_st32(lanes + 32 * j, x);
       }
-      if (!last) {
-        tmem_wait_st();
-        fence_async_smem();
-        tc_fence_before();
-        mbar_arrive(s_ready);
+      tmem_wait_st();
+      fence_async_smem();
+      tc_fence_before();
+      mbar_arrive(s_ready);
+    }
+    // the last state, rounded once, back to the slot through the tile in S_hi's
+    // place (every S^T q has read it)
+    if (final_segment) {
+      if (ok) {
+#pragma unroll 1
+        for (int j = 0; j < DK / 32; ++j) {
+          uint32_t x[32];
+          tmem_ld32(lanes + 32 * j, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            *reinterpret_cast<uint16_t*>(s_s + lp_tile_offset<DK>(32 * j + e, r)) =
+                f32_to_bf16_bits(__uint_as_float(x[e]));
+        }
+      }
+      fence_async_smem();
+      if (named_barrier_and(2, 128, ok) && elected) {
+        for (int x = 0; x < cols / 64; ++x)
+          tma_store_3d(&pool_map, col0 + 64 * x, 0, s * p.H_v + h, smem_addr(s_s + x * DK * 128));
+        bulk_commit_group();
+        bulk_wait_all();
       }
     }
   }
@@ -545,7 +664,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, kLpTmemCols);
   }
@@ -587,10 +706,17 @@ __global__ void __launch_bounds__(kLsThreads, 1)
   const int cols = p.D_v - col0 < kLpCols ? p.D_v - col0 : kLpCols;
   int s, L, n;
   linear_item(p, b, s, L, n);
+  lp_grid_launch_next();
   const int64_t end = static_cast<int64_t>(seg + 1) * prm.seg_chunks * kLpChunk;
   if (L <= end) return;  // the item's last segment, or behind it
-  const int c0 = seg * prm.seg_chunks;
-  const int n_chunks = prm.seg_chunks;
+  // chunks whose weights are all 0 in fp32 add nothing: start behind them
+  const float log_decay = p.log_decay[h];
+  int skip = 0;
+  while (skip < prm.seg_chunks - 1 &&
+         decay_power(log_decay, (prm.seg_chunks - 1 - skip) * kLpChunk) == 0.0f)
+    ++skip;
+  const int c0 = seg * prm.seg_chunks + skip;
+  const int n_chunks = prm.seg_chunks - skip;
 
   extern __shared__ __align__(16) uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
@@ -666,8 +792,7 @@ __global__ void __launch_bounds__(kLsThreads, 1)
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < kLpChunk / 16; ++ks)
-          umma_bf16(tmem, umma_desc_advance(v_mn, ks * 2048), umma_desc_advance(k_mn, ks * 2048),
-                    id_kv, i > 0 || ks > 0);
+          umma_bf16_at(tmem, v_mn, ks * 2048, k_mn, ks * 2048, id_kv, i > 0 || ks > 0);
         umma_commit(free_ + 8 * st);
       }
       if (ok) umma_commit(summed);
@@ -676,7 +801,6 @@ __global__ void __launch_bounds__(kLsThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ weights, store
-    const float log_decay = p.log_decay[h];
     const int r = tid;
     bool ok = true;
     for (int i = 0; i < n_chunks; ++i) {
@@ -693,14 +817,17 @@ __global__ void __launch_bounds__(kLsThreads, 1)
       tc_fence_after();
       const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
       float* dst = prm.starts +
-                   (static_cast<size_t>(tile) * prm.segments + seg + 1) * DK * kLpCols + r;
+                   (static_cast<size_t>(tile) * prm.segments + seg + 1) * DK * kLpCols + 4 * r;
 #pragma unroll 1
       for (int j = 0; j < DK / 32; ++j) {
         uint32_t x[32];
         tmem_ld32(lanes + 32 * j, x);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) dst[(32 * j + e) * kLpCols] = __uint_as_float(x[e]);
+        for (int e = 0; e < 8; ++e)
+          *reinterpret_cast<float4*>(dst + (8 * j + e) * 4 * kLpCols) =
+              make_float4(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1]),
+                          __uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3]));
       }
     }
   }
@@ -724,13 +851,16 @@ __global__ void __launch_bounds__(kLscanThreads) linear_scan_kernel(const Linear
   const LinearParams& p = prm.p;
   const int tile = blockIdx.x / kBlocks;
   const int e = (blockIdx.x % kBlocks) * kLscanThreads + threadIdx.x;
-  const int row = e / kLpCols, col = (tile % prm.slices) * kLpCols + e % kLpCols;
+  const int row = e / (4 * kLpCols) * 4 + e % 4;
+  const int col = (tile % prm.slices) * kLpCols + e / 4 % kLpCols;
   const int bh = tile / prm.slices;
   const int h = bh % p.H_v, b = bh / p.H_v;
   int s, L, n;
   linear_item(p, b, s, L, n);
+  lp_grid_launch_next();
   const int tokens = prm.seg_chunks * kLpChunk;
   const int count = (L + tokens - 1) / tokens;  // segments of this item
+  lp_grid_wait();  // the segments' sums (and, through this launch, for the next one too)
   if (count <= 1) return;
   const float decay = decay_power(p.log_decay[h], tokens);
   float* at = prm.starts + static_cast<size_t>(tile) * prm.segments * DK * kLpCols + e;

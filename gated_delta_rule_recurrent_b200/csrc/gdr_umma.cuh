@@ -96,15 +96,43 @@ __device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
-// As umma_bf16 with A in tensor memory at `a_tmem`: M lanes, two bf16 values of
-// K a 32-bit column (the lower K in the low half), 8 columns an instruction.
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                             uint32_t idesc, bool accumulate) {
+// umma_bf16 with descriptors `a_off` and `b_off` bytes (multiples of 16) behind
+// a_desc and b_desc. The sums are formed next to the MMA, in the low words (a
+// start address has 14 bits, so nothing carries): an unrolled run of them keeps
+// two descriptors in registers, not two for each instruction.
+__device__ __forceinline__ void umma_bf16_at(uint32_t d_tmem, uint64_t a_desc, uint32_t a_off,
+                                             uint64_t b_desc, uint32_t b_off, uint32_t idesc,
+                                             bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b32 al, ah, bl, bh;\n\t.reg .b64 a, b;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      "mov.b64 {al, ah}, %1;\n\t"
+      "mov.b64 {bl, bh}, %2;\n\t"
+      "add.u32 al, al, %5;\n\t"
+      "add.u32 bl, bl, %6;\n\t"
+      "mov.b64 a, {al, ah};\n\t"
+      "mov.b64 b, {bl, bh};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)),
+      "r"(a_off >> 4), "r"(b_off >> 4)
+      : "memory");
+}
+// The same with A in tensor memory at `a_tmem`: M lanes, two bf16 values of K a
+// 32-bit column (the lower K in the low half), 8 columns an instruction.
+// With `run` false nothing is issued.
+__device__ __forceinline__ void umma_bf16_ts_at(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                                uint32_t b_off, uint32_t idesc, bool accumulate,
+                                                bool run) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 bl, bh;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "mov.b64 {bl, bh}, %2;\n\t"
+      "add.u32 bl, bl, %5;\n\t"
+      "mov.b64 b, {bl, bh};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)),
+      "r"(b_off >> 4), "r"(static_cast<uint32_t>(run))
       : "memory");
 }
 
@@ -154,6 +182,17 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
         "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+// As tmem_ld32 for 16 columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
 }
