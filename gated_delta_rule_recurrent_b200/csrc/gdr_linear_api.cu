@@ -102,37 +102,7 @@ gdr::LinearParams linear_params(const gdr_dims* d, const gdr_bf16* query, const 
   return p;
 }
 
-// ---------------------------------------------------------------- decode
-
-template <int DK, int RS>
-int launch_one(const gdr::LinearParams& p, cudaStream_t stream) {
-  constexpr int per_block = gdr::kLinOneThreads / 32 / RS;
-  const int n_tiles = p.B * p.H_v * (p.D_v / 64);
-  const int grid = (n_tiles - 1) / per_block + 1;
-  gdr::linear_decode_one_kernel<DK, RS><<<grid, gdr::kLinOneThreads, 0, stream>>>(p, n_tiles);
-  return launched("linear decode", GDR_KERNEL_LINEAR_DECODE, DK, 64, GDR_LAYOUT_KV, grid,
-                  gdr::kLinOneThreads, 0, RS);
-}
-
-template <int DK>
-int launch_linear_decode(const gdr::LinearParams& p, int sms, cudaStream_t stream) {
-  if (p.T == 1) {
-    const long long tiles = static_cast<long long>(p.B) * p.H_v * (p.D_v / 64);
-    if (tiles < 8LL * sms) return launch_one<DK, 4>(p, stream);
-    return launch_one<DK, 1>(p, stream);
-  }
-  // warps of a block: the largest number up to 8 that shares the head's
-  // 32-column tiles evenly
-  const int tiles = p.D_v / 32;
-  int warps = gdr::kLinManyMaxThreads / 32;
-  while (tiles % warps != 0) --warps;
-  const int grid = p.B * p.H_v;
-  gdr::linear_decode_many_kernel<DK><<<grid, 32 * warps, 0, stream>>>(p);
-  return launched("linear decode", GDR_KERNEL_LINEAR_DECODE, DK, 32, GDR_LAYOUT_KV, grid,
-                  32 * warps, 0, 0);
-}
-
-// ---------------------------------------------------------------- prefill
+// ---------------------------------------------------------------- launches
 
 // [groups, T, D] bf16 as boxes of 64 columns x `rows` rows of one group.
 int encode_rows_map(const gdr_bf16* base, int D, int T, long long groups, int rows,
@@ -153,6 +123,62 @@ int encode_rows_map(const gdr_bf16* base, int D, int T, long long groups, int ro
   return GDR_OK;
 }
 
+template <typename K>
+int opt_in_smem(K kernel, int smem, const gdr_host::Device& dev, std::atomic<bool>* ready) {
+  if (smem > dev.smem_optin)
+    return fail(GDR_ERR_UNSUPPORTED, "prefill tile does not fit in shared memory");
+  if (ready[dev.ordinal].load(std::memory_order_acquire)) return GDR_OK;
+  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (err == cudaSuccess)
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
+  if (err != cudaSuccess)
+    return fail(GDR_ERR_CUDA, std::string("kernel attributes: ") + cudaGetErrorString(err));
+  ready[dev.ordinal].store(true, std::memory_order_release);
+  return GDR_OK;
+}
+
+// ---------------------------------------------------------------- decode
+
+#ifndef GDR_LD_BLOCKS_PER_SM
+#define GDR_LD_BLOCKS_PER_SM 4
+#endif
+
+template <int DK>
+int launch_linear_decode(const gdr::LinearParams& p, const gdr_host::Device& dev,
+                         cudaStream_t stream) {
+  using Shape = gdr::LdShape<DK>;
+  static std::atomic<bool> ready[kMaxDevices];
+  auto kernel = gdr::linear_decode_kernel<DK>;
+  int rc = opt_in_smem(kernel, Shape(Shape::kMaxCols, gdr::kMaxT).smem(), dev, ready);
+  CUtensorMap pool_map;
+  if (rc == GDR_OK)
+    rc = encode_rows_map(p.state_pool, p.D_v, DK, static_cast<long long>(p.pool_size) * p.H_v, DK,
+                         &pool_map);
+  if (rc != GDR_OK) return rc;
+  // the widest part that still gives every SM GDR_LD_BLOCKS_PER_SM blocks
+  const long long heads = static_cast<long long>(p.B) * p.H_v;
+  int cols = Shape::kMaxCols;
+  while (cols > 64 && (cols >= 2 * p.D_v ||
+                       heads * ((p.D_v - 1) / cols + 1) <
+                           static_cast<long long>(GDR_LD_BLOCKS_PER_SM) * dev.sms))
+    cols /= 2;
+  const int parts = (p.D_v - 1) / cols + 1;
+  const int grid = static_cast<int>(heads) * parts;
+  const int smem = Shape(cols, p.T).smem();
+  gdr::LinearDecodeParams prm{};
+  prm.p = p;
+  prm.part_cols = cols;
+  prm.parts = gdr::FastDiv::by(static_cast<uint32_t>(parts));
+  prm.heads = gdr::FastDiv::by(static_cast<uint32_t>(p.H_v));
+  prm.group = gdr::FastDiv::by(static_cast<uint32_t>(p.group));
+  kernel<<<grid, gdr::kLdThreads, smem, stream>>>(pool_map, prm);
+  return launched("linear decode", GDR_KERNEL_LINEAR_DECODE, DK, cols, GDR_LAYOUT_KV, grid,
+                  gdr::kLdThreads, smem, 1);
+}
+
+// ---------------------------------------------------------------- prefill
+
 // How a call's chunks are cut: `segments` per tile of `seg_chunks` chunks.
 struct Segments {
   int slices = 1, segments = 1, seg_chunks = 1;
@@ -171,21 +197,6 @@ Segments plan_segments(const gdr_dims* d, int sms) {
   s.segments = (chunks - 1) / s.seg_chunks + 1;
   s.workspace = tiles * s.segments * d->D_k * gdr::kLpCols * 4;
   return s;
-}
-
-template <typename K>
-int opt_in_smem(K kernel, int smem, const gdr_host::Device& dev, std::atomic<bool>* ready) {
-  if (smem > dev.smem_optin)
-    return fail(GDR_ERR_UNSUPPORTED, "prefill tile does not fit in shared memory");
-  if (ready[dev.ordinal].load(std::memory_order_acquire)) return GDR_OK;
-  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (err == cudaSuccess)
-    err = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                               cudaSharedmemCarveoutMaxShared);
-  if (err != cudaSuccess)
-    return fail(GDR_ERR_CUDA, std::string("kernel attributes: ") + cudaGetErrorString(err));
-  ready[dev.ordinal].store(true, std::memory_order_release);
-  return GDR_OK;
 }
 
 // A launch that, with `overlap`, may start before the one ahead of it on the
@@ -337,8 +348,8 @@ GDR_API int gdr_linear_attention_decode(const gdr_dims* dims, const gdr_bf16* qu
       linear_params(dims, query, key, value, log_decay, state_pool, actual_seq_lengths,
                     ssm_state_indices, num_accepted_tokens, scale_value, out);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return dims->D_k == 64 ? launch_linear_decode<64>(p, dev.sms, st)
-                         : launch_linear_decode<128>(p, dev.sms, st);
+  return dims->D_k == 64 ? launch_linear_decode<64>(p, dev, st)
+                         : launch_linear_decode<128>(p, dev, st);
 }
 
 GDR_API int gdr_linear_attention_prefill_workspace(const gdr_dims* dims, int64_t* bytes) {
