@@ -25,5 +25,6 @@ def __getattr__(name):
     if name in _LAZY:
         from . import binding
 
-        return getattr(binding, name)
+        value = globals()[name] = getattr(binding, name)  # found directly from now on
+        return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

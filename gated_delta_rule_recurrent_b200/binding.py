@@ -387,35 +387,62 @@ def linear_attention_gate(a: torch.Tensor, dt_bias: torch.Tensor, decay_scale: t
     return decay, beta
 
 
+def _is(t, dtype: torch.dtype, shape: tuple, index: int) -> bool:
+    """Whether t is a contiguous tensor of that type and shape on CUDA device ``index``: the
+    conditions of ``_need``, which names the one that fails."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == index and t.is_contiguous())
+
+
+def _call(index: int, fn, *args) -> None:
+    """The library's ``fn(*args)`` with CUDA device ``index`` as the current one."""
+    if torch.cuda.current_device() == index:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args)
+    if rc != 0:
+        _check(rc)
+
+
+# The handle of a device's current stream, without the Stream object around it
+# where this torch has the function.
+_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _linear_args(query, key, value, log_decay, state_pool, actual_seq_lengths,
                  ssm_state_indices, num_accepted_tokens, out):
     if not isinstance(query, torch.Tensor) or query.dim() != 4:
         raise RuntimeError("query must be a 4-D tensor [B, H_qk, T, D_k]")
-    device = query.device
-    if device.type != "cuda":
+    if not query.is_cuda:
         raise RuntimeError("all tensors must be on a CUDA device")
     if not isinstance(value, torch.Tensor) or value.dim() != 4:
         raise RuntimeError("value must be a 4-D tensor [B, H_v, T, D_v]")
     if not isinstance(state_pool, torch.Tensor) or state_pool.dim() != 4:
         raise RuntimeError("state_pool must be a 4-D tensor [pool, H_v, D_k, D_v]")
-    B, H_qk, T, D_k = query.shape
-    H_v, D_v = value.shape[1], value.shape[3]
+    index = query.get_device()
+    B, H_qk, T, D_k = qk = tuple(query.shape)
+    vo = value.shape
+    H_v, D_v = vo[1], vo[3]
+    P = state_pool.shape[0]
     bf16, i32 = torch.bfloat16, torch.int32
-    _need(query, "query", bf16, (B, H_qk, T, D_k), device)
-    _need(key, "key", bf16, (B, H_qk, T, D_k), device)
-    _need(value, "value", bf16, (B, H_v, T, D_v), device)
-    _need(log_decay, "log_decay", torch.float32, (H_v,), device)
-    _need(state_pool, "state_pool", bf16, (state_pool.shape[0], H_v, D_k, D_v), device)
-    _need(actual_seq_lengths, "actual_seq_lengths", i32, (B,), device)
-    _need(ssm_state_indices, "ssm_state_indices", i32, (B,), device)
-    if num_accepted_tokens is not None:
-        _need(num_accepted_tokens, "num_accepted_tokens", i32, (B,), device)
+    wanted = ((query, "query", bf16, qk), (key, "key", bf16, qk),
+              (value, "value", bf16, (B, H_v, T, D_v)),
+              (log_decay, "log_decay", torch.float32, (H_v,)),
+              (state_pool, "state_pool", bf16, (P, H_v, D_k, D_v)),
+              (actual_seq_lengths, "actual_seq_lengths", i32, (B,)),
+              (ssm_state_indices, "ssm_state_indices", i32, (B,)))
+    for t, name, dtype, shape in wanted:
+        if not _is(t, dtype, shape, index):
+            _need(t, name, dtype, shape, query.device)
+    if num_accepted_tokens is not None and not _is(num_accepted_tokens, i32, (B,), index):
+        _need(num_accepted_tokens, "num_accepted_tokens", i32, (B,), query.device)
     if out is None:
-        out = torch.empty((B, H_v, T, D_v), dtype=bf16, device=device)
-    else:
-        _need(out, "out", bf16, (B, H_v, T, D_v), device)
-    dims = Dims(B, T, H_qk, H_v, D_k, D_v, state_pool.shape[0], 0)
-    return device, dims, out
+        out = torch.empty_like(value)
+    elif not _is(out, bf16, vo, index):
+        _need(out, "out", bf16, vo, query.device)
+    return index, Dims(B, T, H_qk, H_v, D_k, D_v, P, 0), out
 
 
 def linear_attention_decode(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
@@ -433,16 +460,14 @@ def linear_attention_decode(query: torch.Tensor, key: torch.Tensor, value: torch
     update of ``state_pool`` (the second result), as for ``decode``. Queued on
     the current CUDA stream; no synchronisation.
     """
-    device, dims, out = _linear_args(query, key, value, log_decay, state_pool,
-                                     actual_seq_lengths, ssm_state_indices,
-                                     num_accepted_tokens, out)
-    with torch.cuda.device(device):
-        stream = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-        rc = lib().gdr_linear_attention_decode(
-            ctypes.byref(dims), _ptr(query), _ptr(key), _ptr(value), _ptr(log_decay),
-            _ptr(state_pool), _ptr(actual_seq_lengths), _ptr(ssm_state_indices),
-            _ptr(num_accepted_tokens), float(scale_value), _ptr(out), stream)
-    _check(rc)
+    index, dims, out = _linear_args(query, key, value, log_decay, state_pool,
+                                    actual_seq_lengths, ssm_state_indices,
+                                    num_accepted_tokens, out)
+    accepted = None if num_accepted_tokens is None else num_accepted_tokens.data_ptr()
+    _call(index, lib().gdr_linear_attention_decode, ctypes.byref(dims), query.data_ptr(),
+          key.data_ptr(), value.data_ptr(), log_decay.data_ptr(), state_pool.data_ptr(),
+          actual_seq_lengths.data_ptr(), ssm_state_indices.data_ptr(), accepted,
+          float(scale_value), out.data_ptr(), _stream(index))
     return out, state_pool
 
 
@@ -456,22 +481,22 @@ def linear_attention_prefill(query: torch.Tensor, key: torch.Tensor, value: torc
     cores). All valid tokens are committed. Queued on the current CUDA stream;
     no synchronisation.
     """
-    device, dims, out = _linear_args(query, key, value, log_decay, state_pool,
-                                     actual_seq_lengths, ssm_state_indices, None, out)
-    with torch.cuda.device(device):
-        stream = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-        need = ctypes.c_int64(0)
-        _check(lib().gdr_linear_attention_prefill_workspace(ctypes.byref(dims),
-                                                            ctypes.byref(need)))
-        # a workspace of this call's own: the allocator gives it to no other
-        # stream or graph while the call runs
-        work = None if need.value == 0 else torch.empty(need.value, dtype=torch.uint8,
-                                                        device=device)
-        rc = lib().gdr_linear_attention_prefill(
-            ctypes.byref(dims), _ptr(query), _ptr(key), _ptr(value), _ptr(log_decay),
-            _ptr(state_pool), _ptr(actual_seq_lengths), _ptr(ssm_state_indices),
-            float(scale_value), _ptr(out), _ptr(work), need.value, stream)
-    _check(rc)
+    index, dims, out = _linear_args(query, key, value, log_decay, state_pool,
+                                    actual_seq_lengths, ssm_state_indices, None, out)
+    L = lib()
+    need = ctypes.c_int64(0)
+    _call(index, L.gdr_linear_attention_prefill_workspace, ctypes.byref(dims),
+          ctypes.byref(need))
+    # a workspace of this call's own: the allocator gives it to no other stream
+    # or graph while the call runs
+    size, work, at = need.value, None, None
+    if size:
+        work = torch.empty(size, dtype=torch.uint8, device=query.device)
+        at = work.data_ptr()
+    _call(index, L.gdr_linear_attention_prefill, ctypes.byref(dims), query.data_ptr(),
+          key.data_ptr(), value.data_ptr(), log_decay.data_ptr(), state_pool.data_ptr(),
+          actual_seq_lengths.data_ptr(), ssm_state_indices.data_ptr(), float(scale_value),
+          out.data_ptr(), at, size, _stream(index))
     return out, state_pool
 
 
@@ -485,24 +510,28 @@ def _cache_args(state_pool, ssm_state_indices, cache, scales, cache_indices):
         if not isinstance(t, torch.Tensor) or t.dim() != 4:
             raise RuntimeError(f"{name} must be a 4-D tensor ([pool or entries, H_v, rows, "
                                "columns])")
-    device = state_pool.device
-    if device.type != "cuda":
+    if not state_pool.is_cuda:
         raise RuntimeError("all tensors must be on a CUDA device")
-    P, H, R, C = state_pool.shape
+    index = state_pool.get_device()
+    P, H, R, C = slots = tuple(state_pool.shape)
     N = cache.shape[0]
-    if cache.dtype not in _CACHE_TYPES:
+    kind = _CACHE_TYPES.get(cache.dtype)
+    if kind is None:
         raise RuntimeError(f"cache must be int8 or float8_e4m3fn, got {cache.dtype}")
     if C % _CACHE_GROUP != 0:
         raise RuntimeError("state_pool's last axis must be a multiple of 64")
     if not isinstance(ssm_state_indices, torch.Tensor) or ssm_state_indices.dim() != 1:
         raise RuntimeError("ssm_state_indices must be a 1-D tensor")
     n = ssm_state_indices.shape[0]
-    _need(state_pool, "state_pool", torch.bfloat16, (P, H, R, C), device)
-    _need(cache, "cache", cache.dtype, (N, H, R, C), device)
-    _need(scales, "scales", torch.float32, (N, H, R, C // _CACHE_GROUP), device)
-    _need(ssm_state_indices, "ssm_state_indices", torch.int32, (n,), device)
-    _need(cache_indices, "cache_indices", torch.int32, (n,), device)
-    return device, P, N, n, H * R * C, _CACHE_TYPES[cache.dtype]
+    for t, name, dtype, shape in (
+            (state_pool, "state_pool", torch.bfloat16, slots),
+            (cache, "cache", cache.dtype, (N, H, R, C)),
+            (scales, "scales", torch.float32, (N, H, R, C // _CACHE_GROUP)),
+            (ssm_state_indices, "ssm_state_indices", torch.int32, (n,)),
+            (cache_indices, "cache_indices", torch.int32, (n,))):
+        if not _is(t, dtype, shape, index):
+            _need(t, name, dtype, shape, state_pool.device)
+    return index, P, N, n, H * R * C, kind
 
 
 def state_quantize(state_pool: torch.Tensor, ssm_state_indices: torch.Tensor,
@@ -518,14 +547,11 @@ def state_quantize(state_pool: torch.Tensor, ssm_state_indices: torch.Tensor,
     values share a scale. Returns (cache, scales). Queued on the current CUDA
     stream; no synchronisation.
     """
-    device, P, N, n, values, kind = _cache_args(state_pool, ssm_state_indices, cache, scales,
-                                                cache_indices)
-    with torch.cuda.device(device):
-        stream = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-        rc = lib().gdr_state_quantize(_ptr(state_pool), P, _ptr(ssm_state_indices), _ptr(cache),
-                                      _ptr(scales), N, _ptr(cache_indices), n, values, kind,
-                                      stream)
-    _check(rc)
+    index, P, N, n, values, kind = _cache_args(state_pool, ssm_state_indices, cache, scales,
+                                               cache_indices)
+    _call(index, lib().gdr_state_quantize, state_pool.data_ptr(), P,
+          ssm_state_indices.data_ptr(), cache.data_ptr(), scales.data_ptr(), N,
+          cache_indices.data_ptr(), n, values, kind, _stream(index))
     return cache, scales
 
 
@@ -537,12 +563,9 @@ def state_dequantize(cache: torch.Tensor, scales: torch.Tensor, cache_indices: t
     The tensors are those of ``state_quantize``. Returns ``state_pool``, updated
     in place. Queued on the current CUDA stream; no synchronisation.
     """
-    device, P, N, n, values, kind = _cache_args(state_pool, ssm_state_indices, cache, scales,
-                                                cache_indices)
-    with torch.cuda.device(device):
-        stream = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-        rc = lib().gdr_state_dequantize(_ptr(cache), _ptr(scales), N, _ptr(cache_indices),
-                                        _ptr(state_pool), P, _ptr(ssm_state_indices), n, values,
-                                        kind, stream)
-    _check(rc)
+    index, P, N, n, values, kind = _cache_args(state_pool, ssm_state_indices, cache, scales,
+                                               cache_indices)
+    _call(index, lib().gdr_state_dequantize, cache.data_ptr(), scales.data_ptr(), N,
+          cache_indices.data_ptr(), state_pool.data_ptr(), P, ssm_state_indices.data_ptr(), n,
+          values, kind, _stream(index))
     return state_pool

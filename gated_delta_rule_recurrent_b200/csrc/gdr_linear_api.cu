@@ -277,9 +277,10 @@ int check_cache(const void* pool, int32_t pool_size, const int32_t* slots, const
     return fail(GDR_ERR_DIMS, "slot_values must be a positive multiple of 64");
   if (type != GDR_CACHE_INT8 && type != GDR_CACHE_E4M3)
     return fail(GDR_ERR_UNSUPPORTED, "cache type must be GDR_CACHE_INT8 or GDR_CACHE_E4M3");
-  const long long blocks = (slot_values - 1) / gdr::kCacheBlockValues + 1;
+  // the most blocks either form needs
+  const long long blocks = (slot_values - 1) / (gdr::kCacheThreads * gdr::kCacheAheadFew * 8) + 1;
   if (blocks > kMaxGrid || blocks * n > kMaxGrid)
-    return fail(GDR_ERR_DIMS, "n * slot_values / 8192 exceeds 2^31 - 1");
+    return fail(GDR_ERR_DIMS, "n * slot_values / 2048 exceeds 2^31 - 1");
   const long long most = pool_size > cache_size ? pool_size : cache_size;
   if (slot_values > (1LL << 61) / most)
     return fail(GDR_ERR_DIMS, "pool or cache exceeds 2^61 values");
@@ -296,8 +297,30 @@ int check_cache(const void* pool, int32_t pool_size, const int32_t* slots, const
   p->slot_values = slot_values;
   p->pool_size = pool_size;
   p->cache_size = cache_size;
-  p->blocks_per_slot = static_cast<int>(blocks);
   return GDR_OK;
+}
+
+// Launches the form of a cache kernel that fits the call: 8 pieces a lane where
+// that still gives every SM GDR_CACHE_BLOCKS_PER_SM blocks.
+#ifndef GDR_CACHE_BLOCKS_PER_SM
+#define GDR_CACHE_BLOCKS_PER_SM 8
+#endif
+template <typename K>
+int launch_cache(K many, K few, const char* what, gdr::CacheParams p, int n,
+                 gdr_stream_t stream) {
+  gdr_host::Device dev;
+  const int rc = gdr_host::current_device(&dev);
+  if (rc != GDR_OK) return rc;
+  const auto blocks = [&](int ahead) {
+    return (p.slot_values - 1) / (gdr::kCacheThreads * ahead * 8) + 1;
+  };
+  const bool is_few = blocks(gdr::kCacheAhead) * n < GDR_CACHE_BLOCKS_PER_SM * dev.sms;
+  p.blocks_per_slot =
+      static_cast<int>(blocks(is_few ? gdr::kCacheAheadFew : gdr::kCacheAhead));
+  const int grid = n * p.blocks_per_slot;
+  (is_few ? few : many)<<<grid, gdr::kCacheThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  return launched(what, GDR_KERNEL_STATE_CACHE, 0, 0, GDR_LAYOUT_KV, grid, gdr::kCacheThreads, 0,
+                  0);
 }
 
 }  // namespace
@@ -405,14 +428,12 @@ GDR_API int gdr_state_quantize(const gdr_bf16* state_pool, int32_t pool_size,
   const int rc = check_cache(state_pool, pool_size, ssm_state_indices, cache, scales, cache_size,
                              cache_indices, n, slot_values, cache_type, &p);
   if (rc != GDR_OK || n == 0) return rc;
-  const int grid = n * p.blocks_per_slot;
-  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  constexpr int many = gdr::kCacheAhead, few = gdr::kCacheAheadFew;
   if (cache_type == GDR_CACHE_E4M3)
-    gdr::state_quantize_kernel<true><<<grid, gdr::kCacheThreads, 0, st>>>(p);
-  else
-    gdr::state_quantize_kernel<false><<<grid, gdr::kCacheThreads, 0, st>>>(p);
-  return launched("state quantize", GDR_KERNEL_STATE_CACHE, 0, 0, GDR_LAYOUT_KV, grid,
-                  gdr::kCacheThreads, 0, 0);
+    return launch_cache(gdr::state_quantize_kernel<true, many>, gdr::state_quantize_kernel<true, few>,
+                        "state quantize", p, n, stream);
+  return launch_cache(gdr::state_quantize_kernel<false, many>, gdr::state_quantize_kernel<false, few>,
+                      "state quantize", p, n, stream);
 }
 
 GDR_API int gdr_state_dequantize(const void* cache, const float* scales, int32_t cache_size,
@@ -424,14 +445,12 @@ GDR_API int gdr_state_dequantize(const void* cache, const float* scales, int32_t
   const int rc = check_cache(state_pool, pool_size, ssm_state_indices, cache, scales, cache_size,
                              cache_indices, n, slot_values, cache_type, &p);
   if (rc != GDR_OK || n == 0) return rc;
-  const int grid = n * p.blocks_per_slot;
-  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  constexpr int many = gdr::kCacheAhead, few = gdr::kCacheAheadFew;
   if (cache_type == GDR_CACHE_E4M3)
-    gdr::state_dequantize_kernel<true><<<grid, gdr::kCacheThreads, 0, st>>>(p);
-  else
-    gdr::state_dequantize_kernel<false><<<grid, gdr::kCacheThreads, 0, st>>>(p);
-  return launched("state dequantize", GDR_KERNEL_STATE_CACHE, 0, 0, GDR_LAYOUT_KV, grid,
-                  gdr::kCacheThreads, 0, 0);
+    return launch_cache(gdr::state_dequantize_kernel<true, many>, gdr::state_dequantize_kernel<true, few>,
+                        "state dequantize", p, n, stream);
+  return launch_cache(gdr::state_dequantize_kernel<false, many>, gdr::state_dequantize_kernel<false, few>,
+                      "state dequantize", p, n, stream);
 }
 
 }  // extern "C"

@@ -13,7 +13,11 @@
 // Both kernels move 2 + 1 + 4/64 bytes a value and do little with it, so HBM
 // bounds them: 16 bytes a lane and access, and each block one contiguous piece
 // of one slot (a slot is contiguous whatever its layout, and rows are whole
-// groups in both layouts of the pool).
+// groups in both layouts of the pool). A lane has 8 accesses in flight, 128
+// threads a block: 256 of 512 slots of 64 heads of 64 x 512 written and read
+// back in 500 us (6.6 TB/s; 4 in flight and 256 threads 521 us). Calls too small
+// to fill the SMs that way take 2 accesses a lane and four times the blocks: one
+// such slot, 8.4 us for both calls against 10.5 us.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -26,8 +30,8 @@
 namespace gdr {
 
 constexpr int kCacheGroup = 64;        // values that share a scale
-constexpr int kCacheThreads = 256;
-constexpr int kCacheAhead = 4;         // 16-byte pieces of bf16 a lane takes at once
+constexpr int kCacheThreads = 128;
+constexpr int kCacheAhead = 8, kCacheAheadFew = 2;  // 8-value pieces a lane takes at once
 constexpr float kCacheFloor = 7.888609052210118e-31f;  // 2^-100
 
 struct CacheParams {
@@ -96,29 +100,26 @@ __device__ __forceinline__ void unpack_codes(uint32_t w, float (&f)[4]) {
   }
 }
 
-// A block takes kCacheThreads * kCacheAhead pieces of 8 values; 8 lanes share
-// a group.
-constexpr int kCacheBlockValues = kCacheThreads * kCacheAhead * 8;
-
-template <bool E4M3>
+// A block takes kCacheThreads * AHEAD pieces of 8 values; 8 lanes share a group.
+template <bool E4M3, int AHEAD>
 __global__ void __launch_bounds__(kCacheThreads) state_quantize_kernel(const CacheParams p) {
   constexpr float top = E4M3 ? 448.0f : 127.0f;
   int64_t slot, entry, first;
-  if (!cache_pair(p, &slot, &entry, &first, kCacheBlockValues)) return;
+  if (!cache_pair(p, &slot, &entry, &first, kCacheThreads * AHEAD * 8)) return;
   const uint16_t* src = p.pool + slot * p.slot_values;
   uint8_t* dst = p.codes + entry * p.slot_values;
   float* sdst = p.scales + entry * (p.slot_values / kCacheGroup);
-  uint4 w[kCacheAhead];
-  int64_t at[kCacheAhead];
+  uint4 w[AHEAD];
+  int64_t at[AHEAD];
 #pragma unroll
-  for (int u = 0; u < kCacheAhead; ++u) {
+  for (int u = 0; u < AHEAD; ++u) {
     at[u] = first + (u * kCacheThreads + threadIdx.x) * 8;
     w[u] = make_uint4(0u, 0u, 0u, 0u);
     // a slot is whole groups, so the 8 lanes of a group agree
     if (at[u] < p.slot_values) w[u] = *reinterpret_cast<const uint4*>(src + at[u]);
   }
 #pragma unroll
-  for (int u = 0; u < kCacheAhead; ++u) {
+  for (int u = 0; u < AHEAD; ++u) {
     const uint32_t x[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
     // magnitudes as integers: their order is the values', with inf and NaN on top
     uint32_t m = max_u16x2(max_u16x2(x[0] & 0x7fff7fffu, x[1] & 0x7fff7fffu),
@@ -149,18 +150,18 @@ __global__ void __launch_bounds__(kCacheThreads) state_quantize_kernel(const Cac
   }
 }
 
-template <bool E4M3>
+template <bool E4M3, int AHEAD>
 __global__ void __launch_bounds__(kCacheThreads) state_dequantize_kernel(const CacheParams p) {
   int64_t slot, entry, first;
-  if (!cache_pair(p, &slot, &entry, &first, kCacheBlockValues)) return;
+  if (!cache_pair(p, &slot, &entry, &first, kCacheThreads * AHEAD * 8)) return;
   uint16_t* dst = p.pool + slot * p.slot_values;
   const uint8_t* src = p.codes + entry * p.slot_values;
   const float* ssrc = p.scales + entry * (p.slot_values / kCacheGroup);
-  uint2 w[kCacheAhead];
-  float scale[kCacheAhead];
-  int64_t at[kCacheAhead];
+  uint2 w[AHEAD];
+  float scale[AHEAD];
+  int64_t at[AHEAD];
 #pragma unroll
-  for (int u = 0; u < kCacheAhead; ++u) {
+  for (int u = 0; u < AHEAD; ++u) {
     at[u] = first + (u * kCacheThreads + threadIdx.x) * 8;
     if (at[u] < p.slot_values) {
       w[u] = *reinterpret_cast<const uint2*>(src + at[u]);
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(kCacheThreads) state_dequantize_kernel(const C
     }
   }
 #pragma unroll
-  for (int u = 0; u < kCacheAhead; ++u) {
+  for (int u = 0; u < AHEAD; ++u) {
     if (at[u] >= p.slot_values) break;
     float f[8], g[4];
     unpack_codes<E4M3>(w[u].x, g);
