@@ -179,46 +179,68 @@ int launch_linear_decode(const gdr::LinearParams& p, const gdr_host::Device& dev
 
 // ---------------------------------------------------------------- prefill
 
-// How a call's chunks are cut: `segments` per tile of `seg_chunks` chunks.
-struct Segments {
-  int slices = 1, segments = 1, seg_chunks = 1;
-  int64_t workspace = 0;  // bytes
+// How a call's chunks are spread over the SMs.
+//   more tiles than SMs: each SM takes an equal share of all chunks (`stream`);
+//   a third of the SMs' number of tiles or fewer, and 12 chunks or more: each tile
+//     is cut into `segments`, which costs a pass over k and v;
+//   between: a CTA for each tile.
+struct PrefillPlan {
+  int slices = 1, segments = 1, seg_chunks = 1, grid = 1;
+  bool stream = false;
+  int64_t states = 0;     // bytes of states in the workspace
+  int64_t workspace = 0;  // and of all of it
 };
-Segments plan_segments(const gdr_dims* d, int sms) {
-  Segments s;
+PrefillPlan plan_prefill(const gdr_dims* d, int sms) {
+  PrefillPlan s;
   s.slices = (d->D_v + gdr::kLpCols - 1) / gdr::kLpCols;
   const int chunks = (d->T - 1) / gdr::kLpChunk + 1;
   s.seg_chunks = chunks;
   const long long tiles = static_cast<long long>(d->B) * d->H_v * s.slices;
-  if (3 * tiles > sms || chunks < 12) return s;
-  int n = static_cast<int>(sms / tiles);
-  if (n > chunks / 4) n = chunks / 4;
-  s.seg_chunks = (chunks - 1) / n + 1;
-  s.segments = (chunks - 1) / s.seg_chunks + 1;
-  s.workspace = tiles * s.segments * d->D_k * gdr::kLpCols * 4;
+  const int64_t state = static_cast<int64_t>(d->D_k) * gdr::kLpCols * 4;
+  s.grid = static_cast<int>(tiles);
+  if (tiles > sms && d->B <= gdr::kLpItems && tiles * chunks < kMaxGrid) {
+    s.stream = true;
+    s.grid = sms;
+    s.states = s.grid * state;
+    s.workspace = s.states + s.grid * 4;
+  } else if (3 * tiles <= sms && chunks >= 12) {
+    int n = static_cast<int>(sms / tiles);
+    if (n > chunks / 4) n = chunks / 4;
+    s.seg_chunks = (chunks - 1) / n + 1;
+    s.segments = (chunks - 1) / s.seg_chunks + 1;
+    s.grid = static_cast<int>(tiles) * s.segments;
+    s.states = s.workspace = tiles * s.segments * state;
+  }
   return s;
 }
 
 // A launch that, with `overlap`, may start before the one ahead of it on the
-// stream is done (the kernel waits for that one where it needs its results).
+// stream is done (the kernel waits for that one where it needs its results), or,
+// with `together`, has all its blocks on the GPU at once (they wait for one
+// another).
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), int grid, int threads, int smem, bool overlap,
-                         cudaStream_t stream, const A&... args) {
+cudaError_t launch_with(void (*kernel)(P...), int grid, int threads, int smem, bool overlap,
+                        bool together, cudaStream_t stream, const A&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  if (overlap) {
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+  } else {
+    attr.id = cudaLaunchAttributeCooperative;
+    attr.val.cooperative = 1;
+  }
   cfg.attrs = &attr;
-  cfg.numAttrs = overlap ? 1 : 0;
+  cfg.numAttrs = overlap || together ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <int DK>
-int launch_linear_prefill(const gdr::LinearParams& p, const Segments& cut, float* workspace,
+int launch_linear_prefill(const gdr::LinearParams& p, const PrefillPlan& plan, uint8_t* workspace,
                           const gdr_host::Device& dev, cudaStream_t stream) {
   using Shape = gdr::LpShape<DK>;
   using SegShape = gdr::LsShape<DK>;
@@ -240,29 +262,32 @@ int launch_linear_prefill(const gdr::LinearParams& p, const Segments& cut, float
   if (rc != GDR_OK) return rc;
   gdr::LinearPrefillParams prm{};
   prm.p = p;
-  prm.slices = cut.slices;
-  prm.segments = cut.segments;
-  prm.seg_chunks = cut.seg_chunks;
-  prm.starts = workspace;
-  const int tiles = p.B * p.H_v * cut.slices;
-  const int grid = tiles * cut.segments;
-  prm.by_length = cut.segments == 1 && tiles > dev.sms && p.B > 1 && p.B <= gdr::kLpSortItems;
+  prm.slices = plan.slices;
+  prm.stream = plan.stream;
+  prm.segments = plan.segments;
+  prm.seg_chunks = plan.seg_chunks;
+  prm.starts = reinterpret_cast<float*>(workspace);
+  const int tiles = p.B * p.H_v * plan.slices;
   cudaError_t err = cudaSuccess;
-  if (cut.segments > 1) {
-    seg_kernel<<<tiles * (cut.segments - 1), gdr::kLsThreads, SegShape::kSmem, stream>>>(
+  if (plan.stream) {
+    prm.flags = reinterpret_cast<int*>(workspace + plan.states);
+    err = cudaMemsetAsync(prm.flags, 0, static_cast<size_t>(plan.grid) * 4, stream);
+  } else if (plan.segments > 1) {
+    seg_kernel<<<tiles * (plan.segments - 1), gdr::kLsThreads, SegShape::kSmem, stream>>>(
         k_map, v_map, prm);
     err = cudaGetLastError();
     if (err == cudaSuccess)
-      err = launch_after(gdr::linear_scan_kernel<DK>, tiles * (DK * gdr::kLpCols / gdr::kLscanThreads),
-                         gdr::kLscanThreads, 0, true, stream, prm);
+      err = launch_with(gdr::linear_scan_kernel<DK>,
+                        tiles * (DK * gdr::kLpCols / gdr::kLscanThreads), gdr::kLscanThreads, 0,
+                        true, false, stream, prm);
   }
   if (err == cudaSuccess)
-    err = launch_after(kernel, grid, gdr::kLpThreads, Shape::kSmem, cut.segments > 1, stream, q_map,
-                       k_map, v_map, o_map, pool_map, prm);
+    err = launch_with(kernel, plan.grid, gdr::kLpThreads, Shape::kSmem, plan.segments > 1,
+                      plan.stream, stream, q_map, k_map, v_map, o_map, pool_map, prm);
   if (err != cudaSuccess)
     return fail(GDR_ERR_CUDA, std::string("linear prefill launch: ") + cudaGetErrorString(err));
   return launched("linear prefill", GDR_KERNEL_LINEAR_PREFILL, DK, gdr::kLpCols, GDR_LAYOUT_KV,
-                  grid, gdr::kLpThreads, Shape::kSmem, Shape::kStages);
+                  plan.grid, gdr::kLpThreads, Shape::kSmem, Shape::kStages);
 }
 
 // ---------------------------------------------------------------- 8-bit cache
@@ -383,7 +408,7 @@ GDR_API int gdr_linear_attention_prefill_workspace(const gdr_dims* dims, int64_t
   gdr_host::Device dev;
   rc = gdr_host::current_device(&dev);
   if (rc != GDR_OK) return rc;
-  *bytes = plan_segments(dims, dev.sms).workspace;
+  *bytes = plan_prefill(dims, dev.sms).workspace;
   return GDR_OK;
 }
 
@@ -406,17 +431,17 @@ GDR_API int gdr_linear_attention_prefill(const gdr_dims* dims, const gdr_bf16* q
   gdr_host::Device dev;
   rc = gdr_host::current_device(&dev);
   if (rc != GDR_OK) return rc;
-  const Segments cut = plan_segments(dims, dev.sms);
-  if (cut.workspace > 0 && (workspace == nullptr || workspace_bytes < cut.workspace))
+  const PrefillPlan plan = plan_prefill(dims, dev.sms);
+  if (plan.workspace > 0 && (workspace == nullptr || workspace_bytes < plan.workspace))
     return fail(GDR_ERR_NULL, "workspace is smaller than gdr_linear_attention_prefill_workspace "
                               "asks for");
   const gdr::LinearParams p =
       linear_params(dims, query, key, value, log_decay, state_pool, actual_seq_lengths,
                     ssm_state_indices, nullptr, scale_value, out);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  float* ws = static_cast<float*>(workspace);
-  return dims->D_k == 64 ? launch_linear_prefill<64>(p, cut, ws, dev, st)
-                         : launch_linear_prefill<128>(p, cut, ws, dev, st);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  return dims->D_k == 64 ? launch_linear_prefill<64>(p, plan, ws, dev, st)
+                         : launch_linear_prefill<128>(p, plan, ws, dev, st);
 }
 
 GDR_API int gdr_state_quantize(const gdr_bf16* state_pool, int32_t pool_size,

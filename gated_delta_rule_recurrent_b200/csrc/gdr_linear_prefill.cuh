@@ -62,12 +62,14 @@ namespace gdr {
 constexpr int kLpChunk = 128;              // tokens of a chunk
 constexpr int kLpCols = 128;               // columns of D_v of a CTA
 constexpr int kLpThreads = 512;
-constexpr int kLpSortItems = 256;          // items whose lengths a CTA ranks, at most
-constexpr int kLpRegsFew = 40, kLpRegsMany = 152;  // 128 * 40 + 384 * 152 <= 65536
+constexpr int kLpItems = 256;              // items whose chunks a CTA counts, at most
+constexpr int kLpRegsFew = 56, kLpRegsMany = 152;  // 128 * 56 + 384 * 152 = 65536
 constexpr int kLpBox = kLpChunk * 128;     // bytes of 128 rows x 64 bf16
 constexpr int kLpTmemCols = 512;
 constexpr int kLpTmemP = 0, kLpTmemInter = 128, kLpTmemIntra = 256, kLpTmemState = 384;
-constexpr int kLpBars = 9;                 // besides six per stage
+constexpr int kLpBars = 10;                // besides six per stage and two per work entry
+constexpr int kLpWorks = 4;                // work entries in the ring
+constexpr int kLpReaders = 14;             // warps that read them
 
 template <int DK>
 struct LpShape {
@@ -76,20 +78,96 @@ struct LpShape {
   static constexpr int kStageBytes = (2 * kBoxes + 2) * kLpBox;  // q, k, v
   static constexpr int kStateOff = kStages * kStageBytes;        // bf16 S^T, [128 j][DK]
   static constexpr int kBarOff = kStateOff + kBoxes * kLpBox;
-  static constexpr int kPowOff = kBarOff + 8 * (6 * kStages + kLpBars) + 16;
-  static constexpr int kSmem = 1024 + kPowOff + 4 * (kLpChunk + 1);
+  static constexpr int kPowOff = kBarOff + 8 * (6 * kStages + kLpBars + 2 * kLpWorks) + 16;
+  static constexpr int kWorkOff = kPowOff + 4 * 32;
+  static constexpr int kLenOff = kWorkOff + 64 * kLpWorks;
+  static constexpr int kSmem = 1024 + kLenOff + 4 * (kLpItems + 1);
 };
 
 struct LinearPrefillParams {
   LinearParams p;
   int slices;      // ceil(D_v / 128)
-  int segments;    // of a tile (1: not cut)
+  int stream;      // nonzero: every CTA takes an equal share of all tiles' chunks
+  int segments;    // of a tile (1: not cut), with stream = 0
   int seg_chunks;  // chunks of a segment
-  int by_length;   // nonzero: tiles in the order of their items' lengths, longest first
-  // [tiles, segments, D_k / 4, 128 columns, 4 rows]: entry g >= 1 is the sum of segment
-  // g - 1 after the first pass, the first state of segment g after the scan. Four rows
-  // of a column are one 16-byte access, coalesced over the columns.
+  // States between CTAs, [D_k / 4][128 columns][4 rows] each (four rows of a column
+  // are one 16-byte access, coalesced over the columns). With segments
+  // [tiles][segments]: entry g >= 1 is the sum of segment g - 1 after the first
+  // pass, the first state of segment g after the scan. With stream [CTAs]: what CTA
+  // c hands to CTA c + 1, which may read it once flags[c] is set.
   float* starts;
+  int* flags;
+};
+
+// One stretch of chunks of one tile: n chunks from chunk c0 of (item b, value
+// head h, columns col0 ..), L tokens from there to the item's end. n = 0 ends
+// the CTA's work.
+struct alignas(16) LpWork {
+  int bh, h, qk, col0;        // qk: item and query head
+  int cols, slot_row, c0, n;  // slot_row: slot and value head
+  int L, whole_start, whole_end;  // from the slot's state; to the slot
+  float log_decay;
+  int rest;  // where the walk goes on (LpWalk::hi)
+};
+static_assert(sizeof(LpWork) <= 64, "an entry of the ring");
+
+// The stretches of a CTA in their order. One warp walks them and passes them on
+// to the others through a ring in shared memory, ahead of time (each role doing
+// it for itself cost 4000 cycles a stretch, most of them for fetching code that
+// runs once a stretch).
+//   stream = 0: one, segment blockIdx.x % segments of tile blockIdx.x / segments.
+//   stream = 1: the CTA's share [lo, hi) of all chunks in tile order, last tile
+//     first: a tile that goes on in the next CTA's share comes first, so that its
+//     state is handed over early, and one that began in the share before comes
+//     last, when that state has long been there.
+struct LpWalk {
+  const LinearPrefillParams& prm;
+  const int* before;  // stream: chunks of all items ahead of item b
+  int lo, hi;
+  __device__ __forceinline__ void next(LpWork& w) {
+    w.n = 0;
+    if (hi <= lo) return;
+    const LinearParams& p = prm.p;
+    const int per_item = p.H_v * prm.slices;
+    int tile, chunks;
+    if (prm.stream) {
+      int b0 = 0, b1 = p.B - 1;  // the item of chunk hi - 1
+      while (b0 < b1) {
+        const int m = (b0 + b1 + 1) >> 1;
+        if (before[m] < hi) {
+          b0 = m;
+        } else {
+          b1 = m - 1;
+        }
+      }
+      chunks = (before[b0 + 1] - before[b0]) / per_item;
+      const int in_item = (hi - 1 - before[b0]) / chunks;
+      const int first = before[b0] + in_item * chunks;
+      tile = b0 * per_item + in_item;
+      w.c0 = lo > first ? lo - first : 0;
+      w.n = hi - first - w.c0;
+      hi = first + w.c0;
+    } else {
+      tile = static_cast<int>(blockIdx.x) / prm.segments;
+      w.c0 = lo;
+      w.n = hi - lo;
+      hi = lo;
+    }
+    w.bh = tile / prm.slices;
+    const int b = w.bh / p.H_v;
+    w.h = w.bh - b * p.H_v;
+    w.qk = b * p.H_qk + w.h / p.group;
+    w.col0 = (tile - w.bh * prm.slices) * kLpCols;
+    w.cols = p.D_v - w.col0 < kLpCols ? p.D_v - w.col0 : kLpCols;  // 64 or 128
+    int s, L, n;
+    linear_item(p, b, s, L, n);
+    w.slot_row = s * p.H_v + w.h;
+    w.L = L - w.c0 * kLpChunk;
+    w.whole_start = w.c0 == 0;
+    w.whole_end = w.n * kLpChunk >= w.L;
+    w.log_decay = p.log_decay[w.h];
+    w.rest = hi;
+  }
 };
 
 // Byte offset of 16-byte chunk c (8 bf16) of row r in a [128 rows][64 columns]
@@ -117,18 +195,17 @@ __device__ __forceinline__ void lp_grid_launch_next() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Row r of a chunk's k times `weight`, in place; `keep` false writes zeros. The
+// Row r of a chunk's k times `weight`, in place. The
 // weight is a pair of bf16, w = hi + lo, and k w = k hi + (k lo) one fused bf16
 // operation behind a small product: the rounding of k w itself, and 2^-17 of
 // it, at half the instructions of the way through fp32. With the swizzle, 8
 // lanes (8 rows) touch 8 different groups of banks.
 template <int kBoxes>
-__device__ __forceinline__ void lp_weight_row(uint8_t* k_s, int r, float weight, bool keep) {
+__device__ __forceinline__ void lp_weight_row(uint8_t* k_s, int r, float weight) {
   const __nv_bfloat16 hi = __float2bfloat16_rn(weight);
   const __nv_bfloat16 lo = __float2bfloat16_rn(weight - __bfloat162float(hi));
   const __nv_bfloat162 hi2 = __halves2bfloat162(hi, hi), lo2 = __halves2bfloat162(lo, lo);
-  const uint32_t valid = keep ? 0xffffffffu : 0u;
-#pragma unroll
+#pragma unroll 1
   for (int x = 0; x < kBoxes; ++x) {
     uint4 w[8];
 #pragma unroll
@@ -141,7 +218,7 @@ __device__ __forceinline__ void lp_weight_row(uint8_t* k_s, int r, float weight,
       for (int e = 0; e < 4; ++e) {
         const __nv_bfloat162 k2 = *reinterpret_cast<const __nv_bfloat162*>(&y[e]);
         const __nv_bfloat162 z = __hfma2(k2, hi2, __hmul2(k2, lo2));
-        y[e] = *reinterpret_cast<const uint32_t*>(&z) & valid;
+        y[e] = *reinterpret_cast<const uint32_t*>(&z);
       }
       *reinterpret_cast<uint4*>(k_s + x * kLpBox + lp_swz(r, c)) =
           make_uint4(y[0], y[1], y[2], y[3]);
@@ -177,6 +254,32 @@ __device__ __forceinline__ int lp_tile_offset(int i, int j) {
   return (j >> 6) * DK * 128 + lp_swz(i, (j & 63) >> 3) + (j & 7) * 2;
 }
 
+// The address that `lane` gives to ldmatrix or stmatrix for piece j of a slot's
+// tile: 16 columns (half j & 1 of warp wq's 32) by 16 rows (from 8 (j & ~1)), as
+// four 8 x 8 matrices whose rows are the tile's: columns 0-7 and 8-15 of rows
+// 0-7, then of rows 8-15.
+template <int DK>
+__device__ __forceinline__ int lp_piece_offset(int j, int wq, int lane) {
+  return lp_tile_offset<DK>(8 * (j & ~1) + (lane & 7) + 8 * (lane >> 4),
+                            32 * wq + 16 * (j & 1) + (lane & 8));
+}
+
+// Set `flag` behind this thread's view of memory; wait for it, bounded.
+__device__ __forceinline__ void lp_set_flag(int* flag) {
+  asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(flag), "r"(1) : "memory");
+}
+__device__ __forceinline__ bool lp_wait_flag(const int* flag) {
+  const long long limit = abandonable_wait_limit();
+  const long long t0 = clock64();
+  for (;;) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
+    if (v != 0) return true;
+    if (clock64() - t0 > limit) return false;
+    __nanosleep(64);
+  }
+}
+
 template <int DK>
 __global__ void __launch_bounds__(kLpThreads, 1)
     linear_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
@@ -189,60 +292,14 @@ __global__ void __launch_bounds__(kLpThreads, 1)
   constexpr int kBoxes = Shape::kBoxes, kStages = Shape::kStages;
   const LinearParams& p = prm.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int seg = blockIdx.x % prm.segments;
-  int tile = blockIdx.x / prm.segments;
-  if (prm.by_length) {
-    // more tiles than SMs: the SMs that are done first take the short ones. The
-    // item whose rank among the lengths is this tile's item number:
-    __shared__ int lengths[kLpSortItems], item;
-    int own_length = 0;
-    if (tid < p.B) {
-      int s_, n_;
-      linear_item(p, tid, s_, own_length, n_);
-      lengths[tid] = own_length;
-    }
-    __syncthreads();
-    if (tid < p.B) {
-      int rank = 0;
-      for (int j = 0; j < p.B; ++j)
-        rank += lengths[j] > own_length || (lengths[j] == own_length && j < tid);
-      if (rank == tile / (p.H_v * prm.slices)) item = tid;
-    }
-    __syncthreads();
-    tile = item * p.H_v * prm.slices + tile % (p.H_v * prm.slices);
-  }
-  const int slice = tile % prm.slices;
-  const int bh = tile / prm.slices;
-  const int h = bh % p.H_v, b = bh / p.H_v;
-  const int col0 = slice * kLpCols;
-  const int cols = p.D_v - col0 < kLpCols ? p.D_v - col0 : kLpCols;  // 64 or 128
-  int s, L, n;
-  linear_item(p, b, s, L, n);
-  uint16_t* out = p.out + static_cast<size_t>(bh) * p.T * p.D_v + col0;
-  const int c0 = seg * prm.seg_chunks;  // this CTA's first chunk
-  const int all_chunks = (L + kLpChunk - 1) / kLpChunk;
-  const int own = all_chunks - c0 < prm.seg_chunks ? all_chunks - c0 : prm.seg_chunks;
-  if (own <= 0) {
-    // nothing but padding here: +0.0 (an empty or skipped item's slot is untouched)
-    const int per_row = cols / 8;
-    lp_grid_wait();
-    const int64_t first = static_cast<int64_t>(c0) * kLpChunk;
-    int64_t end = first + static_cast<int64_t>(prm.seg_chunks) * kLpChunk;
-    if (end > p.T) end = p.T;
-    for (int64_t e = first * per_row + tid; e < end * per_row; e += kLpThreads)
-      *reinterpret_cast<uint4*>(out + (e / per_row) * p.D_v + (e % per_row) * 8) =
-          make_uint4(0u, 0u, 0u, 0u);
-    return;
-  }
-  const int n_chunks = own;
-  const bool final_segment = c0 + own == all_chunks;
-  L -= c0 * kLpChunk;  // tokens from here on
 
   extern __shared__ __align__(16) uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Shape::kBarOff);
-  float* pw = reinterpret_cast<float*>(smem + Shape::kPowOff);  // lambda^0 .. lambda^128
+  float* diag = reinterpret_cast<float*>(smem + Shape::kPowOff);  // lambda^0 .. lambda^31
+  LpWork* works = reinterpret_cast<LpWork*>(smem + Shape::kWorkOff);
+  int* before = reinterpret_cast<int*>(smem + Shape::kLenOff);    // stream: see LpWalk
   const uint32_t bar0 = smem_addr(bars);
   const uint32_t q_full = bar0;                    // + 8 st: q landed
   const uint32_t k_full = bar0 + 8 * kStages;      // + 8 st: k landed
@@ -253,27 +310,94 @@ __global__ void __launch_bounds__(kLpThreads, 1)
   const uint32_t bar1 = bar0 + 48 * kStages;
   const uint32_t p_raw = bar1, p_ready = bar1 + 8, k_ready = bar1 + 16, s_ready = bar1 + 24,
                  s_raw = bar1 + 32, o_raw = bar1 + 40, o_free = bar1 + 48, drained = bar1 + 56,
-                 slot_full = bar1 + 64;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 6 * kStages + kLpBars);
+                 slot_full = bar1 + 64, slot_free = bar1 + 72;
+  const uint32_t work_full = bar1 + 8 * kLpBars;     // + 8 e: entry e of the ring written
+  const uint32_t work_free = work_full + 8 * kLpWorks;  // + 8 e: read by everyone
+  uint32_t* tmem_slot =
+      reinterpret_cast<uint32_t*>(bars + 6 * kStages + kLpBars + 2 * kLpWorks);
   volatile int* abort_word = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  // The loader, warp 0's first lane, starts on the first stages ahead of the
-  // set-up of the CTA (they wait for nobody); the rest follows below.
-  const int zq = b * p.H_qk + h / p.group;
+  // this CTA's stretches
+  LpWalk walk{prm, before, 0, 0};
+  if (prm.stream) {
+    int L = 0;
+    if (tid < p.B) {
+      int s_, n_;
+      linear_item(p, tid, s_, L, n_);
+      before[tid + 1] = (L + kLpChunk - 1) / kLpChunk * (p.H_v * prm.slices);
+    }
+    if (tid == 0) before[0] = 0;
+    __syncthreads();
+    if (warp == 0) {  // running sums, 32 items at a time
+      int carry = 0;
+      for (int i = 0; i < p.B; i += 32) {
+        int x = i + lane < p.B ? before[i + lane + 1] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        if (i + lane < p.B) before[i + lane + 1] = carry + x;
+        carry += __shfl_sync(0xffffffffu, x, 31);
+      }
+    }
+    __syncthreads();
+    // equal shares; only the last CTAs' may be short or empty, so that no empty
+    // one stands between two parts of a tile
+    const int all = before[p.B], share = (all - 1) / static_cast<int>(gridDim.x) + 1;
+    const long long lo = static_cast<long long>(share) * blockIdx.x;
+    walk.lo = lo < all ? static_cast<int>(lo) : all;
+    walk.hi = lo + share < all ? static_cast<int>(lo) + share : all;
+  } else {
+    const int tile = blockIdx.x / prm.segments, seg = blockIdx.x % prm.segments;
+    int s_, L, n_;
+    linear_item(p, tile / prm.slices / p.H_v, s_, L, n_);
+    const int chunks = (L + kLpChunk - 1) / kLpChunk;
+    walk.lo = seg * prm.seg_chunks;
+    walk.hi = walk.lo + prm.seg_chunks < chunks ? walk.lo + prm.seg_chunks : chunks;
+  }
+  LpWork w{};
+  // The next stretch from the ring, for the lanes of a warp together; false at the
+  // end, or when it did not come.
+  int n_works = 0;
+  const auto next_work = [&]() {
+    const int e = n_works % kLpWorks;
+    const bool ok =
+        __all_sync(0xffffffffu, mbar_wait_abandonable(work_full + 8 * e, (n_works / kLpWorks) & 1,
+                                                      abort_word, kErrConsumerWait));
+    if (!ok) return false;
+    w = works[e];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(work_free + 8 * e);
+    ++n_works;
+    return w.n > 0;
+  };
+
+  // The loader, warp 0's first lane, starts on the first chunk ahead of the set-up
+  // of the CTA (it waits for nobody); the rest follows below.
+  const bool loads = !test_hold_tile(static_cast<int>(blockIdx.x));
   int issued[3] = {0, 0, 0};  // loads of q, k and v
-  const auto load = [&](int kind, const CUtensorMap* map, int i, int x0, int z, int boxes) {
-    const int st = i % kStages;
+  int slots = 0;              // and of slots
+  const auto load = [&](int kind, const CUtensorMap* map, int c, int x0, int z, int boxes) {
+    const int st = issued[kind] % kStages;
     const uint32_t bar = q_full + 8 * (kind * kStages + st);
-    const uint32_t dst =
-        smem_addr(smem + st * Shape::kStageBytes + kind * kBoxes * kLpBox);
+    const uint32_t dst = smem_addr(smem + st * Shape::kStageBytes + kind * kBoxes * kLpBox);
     mbar_expect_tx(bar, boxes * kLpBox);
+#pragma unroll 1
     for (int x = 0; x < boxes; ++x)
-      tma_load_3d(dst + x * kLpBox, map, x0 + 64 * x, (c0 + i) * kLpChunk, z, bar);
+      tma_load_3d(dst + x * kLpBox, map, x0 + 64 * x, c * kLpChunk, z, bar);
     mbar_arrive(bar);
     ++issued[kind];
   };
-  const float log_decay = p.log_decay[h];
-  const bool loads = tid == 0 && !test_hold_tile(static_cast<int>(blockIdx.x));
+  const auto load_slot = [&]() {  // where S_hi will be
+    mbar_expect_tx(slot_full, w.cols / 64 * DK * 128);
+#pragma unroll 1
+    for (int x = 0; x < w.cols / 64; ++x)
+      tma_load_3d(smem_addr(smem + Shape::kStateOff + x * DK * 128), &pool_map, w.col0 + 64 * x, 0,
+                  w.slot_row, slot_full);
+    mbar_arrive(slot_full);
+    ++slots;
+  };
   if (tid == 0) {
     for (int x = 0; x < 6 * kStages; ++x) mbar_init(bar0 + 8 * x, 1);
     mbar_init(p_raw, 1);
@@ -285,23 +409,24 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     mbar_init(o_free, 128);
     mbar_init(drained, 1);
     mbar_init(slot_full, 1);
+    mbar_init(slot_free, 1);
+    for (int e = 0; e < kLpWorks; ++e) {
+      mbar_init(work_full + 8 * e, 1);
+      mbar_init(work_free + 8 * e, kLpReaders);
+    }
     *abort_word = 0;
     fence_mbar_init();
     fence_async_smem();
-    if (loads) {
-      load(0, &q_map, 0, 0, zq, kBoxes);
-      load(1, &k_map, 0, 0, zq, kBoxes);
-      if (seg == 0) {  // the slot, where S_hi will be
-        mbar_expect_tx(slot_full, cols / 64 * DK * 128);
-        for (int x = 0; x < cols / 64; ++x)
-          tma_load_3d(smem_addr(smem + Shape::kStateOff + x * DK * 128), &pool_map, col0 + 64 * x,
-                      0, s * p.H_v + h, slot_full);
-        mbar_arrive(slot_full);
-      }
-      load(2, &v_map, 0, col0, bh, cols / 64);
+    walk.next(w);
+    works[0] = w;
+    if (loads && w.n > 0) {
+      load(0, &q_map, w.c0, 0, w.qk, kBoxes);
+      load(1, &k_map, w.c0, 0, w.qk, kBoxes);
+      if (w.whole_start) load_slot();
+      load(2, &v_map, w.c0, w.col0, w.bh, w.cols / 64);
     }
+    mbar_arrive(work_full);
   }
-  if (tid >= 128 && tid <= 128 + kLpChunk) pw[tid - 128] = decay_power(log_decay, tid - 128);
   __syncwarp();
   if (warp == 1) {
     tmem_alloc(smem_addr(tmem_slot), kLpTmemCols);
@@ -312,225 +437,316 @@ __global__ void __launch_bounds__(kLpThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  // A role takes the stretches from the ring, and g counts the chunks of all of
+  // them: the stages and the phases of the barriers go by it.
   if (warp < 4) lp_regs_dec<kLpRegsFew>();
   if (warp == 0) {
     // ------------------------------------------------------------ load
-    if (loads) {
-      for (int i = 1; i < n_chunks; ++i) {
-        const int st = i % kStages;
-        const uint32_t use = (i / kStages) & 1;
-        // S_lo of chunk j sits in the k stage of chunk j - 1, that of chunk 0 in
-        // the last stage: that stage is freed once before its first load
-        const uint32_t k_phase = st == kStages - 1 ? use : use ^ 1;
-        if (!mbar_wait_abandonable(q_free + 8 * st, use ^ 1, abort_word, kErrProducerWait)) break;
-        load(0, &q_map, i, 0, zq, kBoxes);
-        if (!mbar_wait_abandonable(k_free + 8 * st, k_phase, abort_word, kErrProducerWait)) break;
-        load(1, &k_map, i, 0, zq, kBoxes);
-        if (!mbar_wait_abandonable(v_free + 8 * st, use ^ 1, abort_word, kErrProducerWait)) break;
-        load(2, &v_map, i, col0, bh, cols / 64);
+    bool ok = true;
+    int g = 0;
+    while (ok && next_work()) {
+      if (lane == 0 && loads) {
+        for (int i = 0; i < w.n; ++i, ++g) {
+          if (g == 0) continue;  // on its way already
+          const int st = g % kStages;
+          const uint32_t use = (g / kStages) & 1;
+          // S_lo of a chunk sits in the k stage of the chunk before it, the very
+          // first in the last stage: that one is freed once before its first load
+          const uint32_t k_phase = st == kStages - 1 ? use : use ^ 1;
+          ok = mbar_wait_abandonable(q_free + 8 * st, use ^ 1, abort_word, kErrProducerWait);
+          if (!ok) break;
+          load(0, &q_map, w.c0 + i, 0, w.qk, kBoxes);
+          ok = mbar_wait_abandonable(k_free + 8 * st, k_phase, abort_word, kErrProducerWait);
+          if (!ok) break;
+          load(1, &k_map, w.c0 + i, 0, w.qk, kBoxes);
+          if (i == 0 && w.whole_start) {  // S_hi's place is free after the stretch before
+            ok = mbar_wait_abandonable(slot_free, (slots & 1) ^ 1, abort_word, kErrProducerWait);
+            if (!ok) break;
+            load_slot();
+          }
+          ok = mbar_wait_abandonable(v_free + 8 * st, use ^ 1, abort_word, kErrProducerWait);
+          if (!ok) break;
+          load(2, &v_map, w.c0 + i, w.col0, w.bh, w.cols / 64);
+        }
       }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (lane == 0) {
       // no copy may outlive the CTA: the last load of every stage has landed
       for (int x = 0; x < 3; ++x)
         for (int i = issued[x] > kStages ? issued[x] - kStages : 0; i < issued[x]; ++i)
           if (!mbar_wait_bounded(q_full + 8 * (x * kStages + i % kStages), (i / kStages) & 1))
             flag_error(kErrDrainWait);
-      if (seg == 0 && !mbar_wait_bounded(slot_full, 0)) flag_error(kErrDrainWait);
+      if (slots > 0 && !mbar_wait_bounded(slot_full, (slots - 1) & 1)) flag_error(kErrDrainWait);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ mma
-    if (lane == 0) {
+    // The warp stays together (descriptors and addresses are uniform), one lane issues.
+    const bool leader = elect_one();
+    {
       constexpr uint32_t id_qk = umma_idesc_bf16<128, 128, false, false>();
       constexpr uint32_t id_pv = umma_idesc_bf16<128, 128, false, true>();
       constexpr uint32_t id_kv = umma_idesc_bf16<128, DK, true, true>();
       const uint64_t s_desc =
           umma_desc(smem_addr(smem + Shape::kStateOff), 16, 1024, kUmmaSwizzle128);
       auto wait = [&](uint32_t bar, uint32_t phase) {
-        const bool done = mbar_wait_abandonable(bar, phase, abort_word, kErrConsumerWait);
+        const bool done = __all_sync(
+            0xffffffffu, mbar_wait_abandonable(bar, phase, abort_word, kErrConsumerWait));
         tc_fence_after();
         return done;
       };
       bool ok = true;
-      for (int i = 0; i < n_chunks; ++i) {
-        const int st = i % kStages;
-        const uint32_t ph = i & 1;
-        const uint32_t q_s = smem_addr(smem + st * Shape::kStageBytes);
-        const uint32_t k_s = q_s + kBoxes * kLpBox, v_s = k_s + kBoxes * kLpBox;
-        const uint64_t q_k = umma_desc(q_s, 16, 1024, kUmmaSwizzle128);
-        const uint64_t k_k = umma_desc(k_s, 16, 1024, kUmmaSwizzle128);
-        const uint64_t k_mn = umma_desc(k_s, kLpBox, 1024, kUmmaSwizzle128);
-        const uint64_t v_mn = umma_desc(v_s, kLpBox, 1024, kUmmaSwizzle128);
-        const uint32_t use = (i / kStages) & 1;
-        if (!wait(q_full + 8 * st, use) || !wait(k_full + 8 * st, use)) break;
-#pragma unroll
-        for (int ks = 0; ks < DK / 16; ++ks) {
-          const uint32_t off = (ks >> 2) * kLpBox + (ks & 3) * 32;
-          umma_bf16_at(tmem + kLpTmemP, q_k, off, k_k, off, id_qk, ks > 0);
-        }
-        umma_commit(p_raw);
-        const bool from_slot = i == 0 && seg == 0;
-        if (!wait(from_slot ? slot_full : s_ready, ph)) break;
-        if (i > 0 && !wait(o_free, ph ^ 1)) break;
-        const int lo_st = (i + kStages - 1) % kStages;  // the k stage that holds S_lo
-        if (from_slot) {
-          // the slot's tile is S itself, rows of 64 columns: the other major-ness,
-          // and bf16 has no S_lo
-          const uint64_t tile_desc =
-              umma_desc(smem_addr(smem + Shape::kStateOff), DK * 128, 1024, kUmmaSwizzle128);
+      int g = 0;
+      while (ok && next_work()) {
+        for (int i = 0; i < w.n; ++i, ++g) {
+          ok = false;  // until the end of the chunk
+          const int st = g % kStages;
+          const uint32_t ph = g & 1;
+          const uint32_t q_s = smem_addr(smem + st * Shape::kStageBytes);
+          const uint32_t k_s = q_s + kBoxes * kLpBox, v_s = k_s + kBoxes * kLpBox;
+          const uint64_t q_k = umma_desc(q_s, 16, 1024, kUmmaSwizzle128);
+          const uint64_t k_k = umma_desc(k_s, 16, 1024, kUmmaSwizzle128);
+          const uint64_t k_mn = umma_desc(k_s, kLpBox, 1024, kUmmaSwizzle128);
+          const uint64_t v_mn = umma_desc(v_s, kLpBox, 1024, kUmmaSwizzle128);
+          const uint32_t use = (g / kStages) & 1;
+          if (!wait(q_full + 8 * st, use) || !wait(k_full + 8 * st, use)) break;
+          if (leader) {
+#pragma unroll 2
+            for (int ks = 0; ks < DK / 16; ++ks) {
+              const uint32_t off = (ks >> 2) * kLpBox + (ks & 3) * 32;
+              umma_bf16_at(tmem + kLpTmemP, q_k, off, k_k, off, id_qk, ks > 0);
+            }
+            umma_commit(p_raw);
+          }
+          __syncwarp();
+          const bool from_slot = i == 0 && w.whole_start;
+          if (!wait(from_slot ? slot_full : s_ready, from_slot ? slots & 1 : ph)) break;
+          if (g > 0 && !wait(o_free, ph ^ 1)) break;
+          const int lo_st = (g + kStages - 1) % kStages;  // the k stage that holds S_lo
+          if (from_slot) ++slots;
+          if (leader) {
+            if (from_slot) {
+              // the slot's tile is S itself, rows of 64 columns: the other major-ness,
+              // and bf16 has no S_lo
+              const uint64_t tile_desc =
+                  umma_desc(smem_addr(smem + Shape::kStateOff), DK * 128, 1024, kUmmaSwizzle128);
 #pragma unroll 1
-          for (int ks = 0; ks < DK / 16; ++ks)
-            umma_bf16_at(tmem + kLpTmemInter, q_k, (ks >> 2) * kLpBox + (ks & 3) * 32, tile_desc,
-                         ks * 2048, id_pv, ks > 0);
-        } else {
-          const uint64_t lo_desc =
-              umma_desc(smem_addr(smem + lo_st * Shape::kStageBytes + kBoxes * kLpBox), 16, 1024,
-                        kUmmaSwizzle128);
-#pragma unroll
-          for (int ks = 0; ks < DK / 16; ++ks) {
-            const uint32_t off = (ks >> 2) * kLpBox + (ks & 3) * 32;
-            umma_bf16_at(tmem + kLpTmemInter, q_k, off, s_desc, off, id_qk, ks > 0);
+              for (int ks = 0; ks < DK / 16; ++ks)
+                umma_bf16_at(tmem + kLpTmemInter, q_k, (ks >> 2) * kLpBox + (ks & 3) * 32,
+                             tile_desc, ks * 2048, id_pv, ks > 0);
+            } else {
+              const uint64_t lo_desc =
+                  umma_desc(smem_addr(smem + lo_st * Shape::kStageBytes + kBoxes * kLpBox), 16,
+                            1024, kUmmaSwizzle128);
+#pragma unroll 1
+              for (int half = 0; half < 2; ++half) {
+                const uint64_t desc = half ? lo_desc : s_desc;
+#pragma unroll 2
+                for (int ks = 0; ks < DK / 16; ++ks) {
+                  const uint32_t off = (ks >> 2) * kLpBox + (ks & 3) * 32;
+                  umma_bf16_at(tmem + kLpTmemInter, q_k, off, desc, off, id_qk,
+                               ks > 0 || half > 0);
+                }
+              }
+            }
+            umma_commit(q_free + 8 * st);
           }
-#pragma unroll
-          for (int ks = 0; ks < DK / 16; ++ks) {
-            const uint32_t off = (ks >> 2) * kLpBox + (ks & 3) * 32;
-            umma_bf16_at(tmem + kLpTmemInter, q_k, off, lo_desc, off, id_qk, true);
+          __syncwarp();
+          // A stretch that starts from its slot: the scaled slot is in TMEM, and the
+          // state of the stretch before has left the k stage in which S_lo would be.
+          if (from_slot && !wait(s_ready, ph)) break;
+          if (leader) umma_commit(k_free + 8 * lo_st);
+          __syncwarp();
+          if (!wait(v_full + 8 * st, use) || !wait(k_ready, ph)) break;
+          if (leader) {
+#pragma unroll 2
+            for (int ks = 0; ks < kLpChunk / 16; ++ks)
+              umma_bf16_at(tmem + kLpTmemState, v_mn, ks * 2048, k_mn, ks * 2048, id_kv, true);
+            umma_commit(s_raw);
           }
+          __syncwarp();
+          // The first time round the instructions of P V are run once with the MMA
+          // switched off, so that fetching them (3500 cycles, cold) falls into the wait.
+          bool p_ok = true;
+          for (int run = g > 0; run < 2; ++run) {
+            if (run) p_ok = wait(p_ready, ph);
+            if (!p_ok) break;
+            if (leader) {
+#pragma unroll 2
+              for (int ks = 0; ks < kLpChunk / 16; ++ks)
+                umma_bf16_ts_at(tmem + kLpTmemIntra, tmem + kLpTmemP + 8 * ks, v_mn, ks * 2048,
+                                id_pv, ks > 0, run != 0);
+            }
+            __syncwarp();
+          }
+          if (!p_ok) break;
+          if (leader) umma_commit(o_raw);
+          __syncwarp();
+          ok = true;
         }
-        umma_commit(q_free + 8 * st);
-        umma_commit(k_free + 8 * lo_st);
-        if (from_slot && !wait(s_ready, ph)) break;  // the scaled slot, in TMEM
-        if (!wait(v_full + 8 * st, use) || !wait(k_ready, ph)) break;
-#pragma unroll
-        for (int ks = 0; ks < kLpChunk / 16; ++ks)
-          umma_bf16_at(tmem + kLpTmemState, v_mn, ks * 2048, k_mn, ks * 2048, id_kv, true);
-        umma_commit(s_raw);
-        // The first time round the instructions of P V are run once with the MMA
-        // switched off, so that fetching them (3500 cycles, cold) falls into the wait.
-        for (int run = i > 0; run < 2; ++run) {
-          if (run && !wait(p_ready, ph)) {
-            ok = false;
-            break;
-          }
-#pragma unroll
-          for (int ks = 0; ks < kLpChunk / 16; ++ks)
-            umma_bf16_ts_at(tmem + kLpTmemIntra, tmem + kLpTmemP + 8 * ks, v_mn, ks * 2048, id_pv,
-                            ks > 0, run != 0);
-        }
-        if (!ok) break;
-        umma_commit(o_raw);
       }
-      umma_commit(drained);
-      if (!mbar_wait_bounded(drained, 0)) flag_error(kErrDrainWait);
+      if (leader) {
+        umma_commit(drained);
+        if (!mbar_wait_bounded(drained, 0)) flag_error(kErrDrainWait);
+      }
     }
-  } else if (warp < 4) {
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ walk
+    if (lane == 0) {
+      w = works[0];  // the first one comes from the loader
+      walk.hi = w.rest;
+      for (int k = 1; w.n > 0; ++k) {
+        const int e = k % kLpWorks;
+        if (!mbar_wait_abandonable(work_free + 8 * e, ((k / kLpWorks) & 1) ^ 1, abort_word,
+                                   kErrProducerWait))
+          break;
+        walk.next(w);
+        works[e] = w;
+        mbar_arrive(work_full + 8 * e);
+      }
+    }
+  } else if (warp == 3) {
     // ------------------------------------------------------------ padding
-    // this CTA's tokens behind the last chunk: +0.0
+    // tokens behind an item's last chunk: +0.0. A tile's own CTA (segment), or
+    // every grid's width of tiles.
     lp_grid_wait();
-    const int per_row = cols / 8;
-    int64_t end = static_cast<int64_t>(c0 + prm.seg_chunks) * kLpChunk;
-    end = (end < p.T ? end : p.T) * per_row;
-    for (int64_t e = static_cast<int64_t>(c0 + n_chunks) * kLpChunk * per_row + (tid - 64);
-         e < end; e += 64)
-      *reinterpret_cast<uint4*>(out + (e / per_row) * p.D_v + (e % per_row) * 8) =
-          make_uint4(0u, 0u, 0u, 0u);
+    const int tiles = p.B * p.H_v * prm.slices;
+    const int step = prm.stream ? static_cast<int>(gridDim.x) : tiles;
+    for (int tile = prm.stream ? blockIdx.x : blockIdx.x / prm.segments; tile < tiles;
+         tile += step) {
+      const int bh = tile / prm.slices, col0 = (tile - bh * prm.slices) * kLpCols;
+      const int sh = p.D_v - col0 < kLpCols ? 3 : 4;  // 16-byte pieces of a row: 8 or 16
+      int s_, L, n_;
+      linear_item(p, bh / p.H_v, s_, L, n_);
+      int64_t from = static_cast<int64_t>((L + kLpChunk - 1) / kLpChunk) * kLpChunk;
+      int64_t to = p.T;
+      if (!prm.stream) {
+        const int64_t first =
+            static_cast<int64_t>(blockIdx.x % prm.segments) * prm.seg_chunks * kLpChunk;
+        const int64_t last = first + static_cast<int64_t>(prm.seg_chunks) * kLpChunk;
+        from = from > first ? from : first;
+        to = to < last ? to : last;
+      }
+      const int rows = 32 >> sh;
+      uint16_t* at = p.out + static_cast<size_t>(bh) * p.T * p.D_v + col0 +
+                     (from + (lane >> sh)) * p.D_v + (lane & ((1 << sh) - 1)) * 8;
+      for (int64_t i = from + (lane >> sh); i < to; i += rows, at += static_cast<size_t>(rows) * p.D_v)
+        *reinterpret_cast<uint4*>(at) = make_uint4(0u, 0u, 0u, 0u);
+    }
   } else if (warp < 8) {
     // ------------------------------------------------------------ P
     lp_regs_inc<kLpRegsMany>();
     const int wq = warp & 3, t = tid & 127;
     const uint32_t base = tmem + kLpTmemP + (static_cast<uint32_t>(32 * wq) << 16);
-    unsigned long long w2[16];  // lambda^{31-e}
+    bool ok = true;
+    int g = 0;
+    while (ok && next_work()) {
+      const float log_decay = w.log_decay;
+      named_barrier(1, 128);  // the weights of the stretch before are no longer read
+      if (wq == 0) diag[lane] = decay_power(log_decay, lane);
+      named_barrier(1, 128);
+      unsigned long long w2[16];  // lambda^{31-e}
 #pragma unroll
-    for (int e = 0; e < 16; ++e) w2[e] = pk(pw[31 - 2 * e], pw[30 - 2 * e]);
-    for (int i = 0; i < n_chunks; ++i) {
-      const bool ok = mbar_wait_abandonable(p_raw, i & 1, abort_word, kErrConsumerWait);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
+      for (int e = 0; e < 16; ++e) w2[e] = pk(diag[31 - 2 * e], diag[30 - 2 * e]);
+      for (int i = 0; i < w.n; ++i, ++g) {
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait_abandonable(p_raw, g & 1, abort_word, kErrConsumerWait));
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll 1
-      for (int j = 0; j < 4; ++j) {
-        uint32_t y[16];
-        if (j <= wq) {
-          uint32_t x[32];
-          tmem_ld32(base + 32 * j, x);
-          tmem_wait_ld();
-          if (j < wq) {
-            // all 32 columns are behind row t: lambda^{t-c} as
-            // lambda^{t-32j-31} lambda^{31-e}, two packed products a pair
-            const float a = pw[t - 32 * j - 31];
-            const unsigned long long a2 = pk(a, a);
+        for (int j = 0; j < 4; ++j) {
+          uint32_t y[16];
+          if (j <= wq) {
+            uint32_t x[32];
+            tmem_ld32(base + 32 * j, x);
+            const float a = decay_power(log_decay, j < wq ? t - 32 * j - 31 : 0);
+            tmem_wait_ld();
+            if (j < wq) {
+              // all 32 columns are behind row t: lambda^{t-c} as
+              // lambda^{t-32j-31} lambda^{31-e}, two packed products a pair
+              const unsigned long long a2 = pk(a, a);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 f = upk(mul2(mul2(pk(__uint_as_float(x[2 * e]),
-                                                __uint_as_float(x[2 * e + 1])), a2), w2[e]));
-              y[e] = pack_bf16x2(f.x, f.y);
+              for (int e = 0; e < 16; ++e) {
+                const float2 f = upk(mul2(mul2(pk(__uint_as_float(x[2 * e]),
+                                                  __uint_as_float(x[2 * e + 1])), a2), w2[e]));
+                y[e] = pack_bf16x2(f.x, f.y);
+              }
+            } else {
+              // the diagonal block: what is ahead of row t is set to 0
+              const float* pt = diag + lane;
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                y[e] = pack_bf16x2(
+                    2 * e <= lane ? __uint_as_float(x[2 * e]) * pt[-2 * e] : 0.0f,
+                    2 * e + 1 <= lane ? __uint_as_float(x[2 * e + 1]) * pt[-2 * e - 1] : 0.0f);
             }
           } else {
-            // the diagonal block: what is ahead of row t is set to 0
-            const float* pt = pw + lane;
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              y[e] = pack_bf16x2(
-                  2 * e <= lane ? __uint_as_float(x[2 * e]) * pt[-2 * e] : 0.0f,
-                  2 * e + 1 <= lane ? __uint_as_float(x[2 * e + 1]) * pt[-2 * e - 1] : 0.0f);
+            for (int e = 0; e < 16; ++e) y[e] = 0u;
           }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = 0u;
+          tmem_st16(base + 16 * j, y);
         }
-        tmem_st16(base + 16 * j, y);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(p_ready);
       }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(p_ready);
+      ok = named_barrier_and(1, 128, ok);
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------ out
     lp_regs_inc<kLpRegsMany>();
     const int wq = warp & 3, t = tid & 127;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * wq) << 16);
-    const float inter = pw[t + 1] * p.scale;
-    const unsigned long long inter2 = pk(inter, inter), scale2 = pk(p.scale, p.scale);
+    const unsigned long long scale2 = pk(p.scale, p.scale);
     const bool elected = t == 0;
-    for (int i = 0; i < n_chunks; ++i) {
-      const int st = i % kStages;
-      const uint32_t valid = t < L - i * kLpChunk ? 0xffffffffu : 0u;  // padding: +0.0
-      uint8_t* o_s = smem + st * Shape::kStageBytes + 2 * kBoxes * kLpBox;
-      const bool ok =
-          __all_sync(0xffffffffu, mbar_wait_abandonable(o_raw, i & 1, abort_word,
-                                                        kErrConsumerWait));
-      if (ok) {
-        tc_fence_after();
+    bool ok = true;
+    int g = 0;
+    while (ok && next_work()) {
+      const float inter = decay_power(w.log_decay, t + 1) * p.scale;
+      const unsigned long long inter2 = pk(inter, inter);
+      for (int i = 0; i < w.n; ++i, ++g) {
+        const int st = g % kStages;
+        const uint32_t valid = t < w.L - i * kLpChunk ? 0xffffffffu : 0u;  // padding: +0.0
+        uint8_t* o_s = smem + st * Shape::kStageBytes + 2 * kBoxes * kLpBox;
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait_abandonable(o_raw, g & 1, abort_word, kErrConsumerWait));
+        if (ok) {
+          tc_fence_after();
 #pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-          uint32_t x[32], z[32];
-          tmem_ld32(lanes + kLpTmemInter + 32 * j, x);
-          tmem_ld32(lanes + kLpTmemIntra + 32 * j, z);
-          tmem_wait_ld();
+          for (int j = 0; j < 4; ++j) {
+            uint32_t x[32], z[32];
+            tmem_ld32(lanes + kLpTmemInter + 32 * j, x);
+            tmem_ld32(lanes + kLpTmemIntra + 32 * j, z);
+            tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t y[4];
+            for (int c = 0; c < 4; ++c) {
+              uint32_t y[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int k = 8 * c + 2 * e;
-              const float2 f = upk(
-                  fma2(pk(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), inter2,
-                       mul2(pk(__uint_as_float(z[k]), __uint_as_float(z[k + 1])), scale2)));
-              y[e] = pack_bf16x2(f.x, f.y) & valid;
+              for (int e = 0; e < 4; ++e) {
+                const int k = 8 * c + 2 * e;
+                const float2 f = upk(
+                    fma2(pk(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), inter2,
+                         mul2(pk(__uint_as_float(z[k]), __uint_as_float(z[k + 1])), scale2)));
+                y[e] = pack_bf16x2(f.x, f.y) & valid;
+              }
+              *reinterpret_cast<uint4*>(o_s + (j >> 1) * kLpBox + lp_swz(t, 4 * (j & 1) + c)) =
+                  make_uint4(y[0], y[1], y[2], y[3]);
             }
-            *reinterpret_cast<uint4*>(o_s + (j >> 1) * kLpBox + lp_swz(t, 4 * (j & 1) + c)) =
-                make_uint4(y[0], y[1], y[2], y[3]);
           }
+          tc_fence_before();
+          mbar_arrive(o_free);
         }
-        tc_fence_before();
-        mbar_arrive(o_free);
-      }
-      fence_async_smem();
-      if (!named_barrier_and(1, 128, ok)) break;
-      if (elected) {
-        for (int x = 0; x < cols / 64; ++x)
-          tma_store_3d(&o_map, col0 + 64 * x, (c0 + i) * kLpChunk, bh,
-                       smem_addr(o_s + x * kLpBox));
-        bulk_commit_group();
-        bulk_wait_read_all();
-        mbar_arrive(v_free + 8 * st);
+        fence_async_smem();
+        ok = named_barrier_and(2, 128, ok);
+        if (!ok) break;
+        if (elected) {
+          for (int x = 0; x < w.cols / 64; ++x)
+            tma_store_3d(&o_map, w.col0 + 64 * x, (w.c0 + i) * kLpChunk, w.bh,
+                         smem_addr(o_s + x * kLpBox));
+          bulk_commit_group();
+          bulk_wait_read_all();
+          mbar_arrive(v_free + 8 * st);
+        }
       }
     }
     if (elected) bulk_wait_all();
@@ -542,122 +758,191 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     uint8_t* s_s = smem + Shape::kStateOff;
     const bool elected = r == 0;
     bool ok = true;
-    // the first state, scaled, into TMEM for the first sum; a segment's as hi and
-    // lo for its first S^T q too (the slot's tile serves that as it is)
-    {
-      const float decay = pw[L < kLpChunk ? L : kLpChunk];
-      const float* start = prm.starts + static_cast<size_t>(blockIdx.x) * DK * kLpCols + 4 * r;
-      uint8_t* lo_s = smem + (kStages - 1) * Shape::kStageBytes + kBoxes * kLpBox;
-      if (seg == 0)
-        ok = __all_sync(0xffffffffu, mbar_wait_abandonable(slot_full, 0, abort_word,
-                                                           kErrConsumerWait));
-#pragma unroll 1
-      for (int j = 0; j < DK / 32; ++j) {
-        uint32_t x[32];
-        if (seg > 0) {
-          if (j == 0) lp_grid_wait();  // the scan's results
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 f = *reinterpret_cast<const float4*>(start + (8 * j + e) * 4 * kLpCols);
-            x[4 * e] = __float_as_uint(f.x);
-            x[4 * e + 1] = __float_as_uint(f.y);
-            x[4 * e + 2] = __float_as_uint(f.z);
-            x[4 * e + 3] = __float_as_uint(f.w);
+    // A state written for the next CTA and not passed on yet: that happens a chunk
+    // or two later, when its writes are done and the fence need not wait for them
+    // (5000 cycles).
+    bool hands = false;
+    const auto pass_on = [&]() {
+      __threadfence();
+      if (named_barrier_and(3, 128, true) && elected) lp_set_flag(prm.flags + blockIdx.x);
+      hands = false;
+    };
+    int g = 0;
+    while (ok && next_work()) {
+      const float log_decay = w.log_decay;
+      // the first state, scaled, into TMEM for the first sum; one that comes from
+      // another CTA as hi and lo for its first S^T q too (a slot's tile serves that
+      // as it is)
+      {
+        const float decay = decay_power(log_decay, w.L < kLpChunk ? w.L : kLpChunk);
+        const float* start = prm.starts + 4 * r +
+                             static_cast<size_t>(prm.stream ? blockIdx.x - 1 : blockIdx.x) * DK *
+                                 kLpCols;
+        uint8_t* lo_s = smem + (g + kStages - 1) % kStages * Shape::kStageBytes + kBoxes * kLpBox;
+        if (w.whole_start) {
+          ok = mbar_wait_abandonable(slot_full, slots & 1, abort_word, kErrConsumerWait);
+          ++slots;
+        } else if (!prm.stream) {
+          lp_grid_wait();  // the scan's results
+        } else if (elected) {
+          ok = lp_wait_flag(prm.flags + blockIdx.x - 1);
+          if (!ok) {
+            flag_error(kErrConsumerWait);
+            *abort_word = 1;
           }
-          lp_store_state(s_s, lo_s, r, j, x);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            x[e] = static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(
-                       s_s + lp_tile_offset<DK>(32 * j + e, r))) << 16;
         }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * decay);
-        tmem_st32(lanes + 32 * j, x);
-      }
-      tmem_wait_st();
-      fence_async_smem();
-      tc_fence_before();
-      if (ok) mbar_arrive(s_ready);
-    }
-    for (int i = 0; i < n_chunks; ++i) {
-      const int st = i % kStages;
-      const uint32_t use = (i / kStages) & 1;
-      const int left = L - i * kLpChunk;
-      const int Lc = left < kLpChunk ? left : kLpChunk;
-      uint8_t* k_s = smem + st * Shape::kStageBytes + kBoxes * kLpBox;
-      uint8_t* v_s = k_s + kBoxes * kLpBox;
-      // q k^T has read k (and waited for it to land)
-      ok = ok && mbar_wait_abandonable(k_full + 8 * st, use, abort_word, kErrConsumerWait) &&
-           mbar_wait_abandonable(p_raw, i & 1, abort_word, kErrConsumerWait);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      lp_weight_row<kBoxes>(k_s, r, r < Lc ? pw[Lc - 1 - r] : 0.0f, r < Lc);
-      if (Lc < kLpChunk) {  // rows of v behind the last token: zeros
-        ok = __all_sync(0xffffffffu, mbar_wait_abandonable(v_full + 8 * st, use, abort_word,
-                                                           kErrConsumerWait));
+        ok = named_barrier_and(3, 128, ok);
         if (!ok) break;
-        if (r >= Lc) {
-#pragma unroll
-          for (int c = 0; c < 16; ++c)
-            *reinterpret_cast<uint4*>(v_s + (c >> 3) * kLpBox + lp_swz(r, c & 7)) =
-                make_uint4(0u, 0u, 0u, 0u);
-        }
-      }
-      fence_async_smem();
-      mbar_arrive(k_ready);
-
-      // the sum is done and has read this chunk's k: its stage takes S_lo
-      ok = __all_sync(0xffffffffu,
-                      mbar_wait_abandonable(s_raw, i & 1, abort_word, kErrConsumerWait));
-      if (!ok) break;
-      tc_fence_after();
-      if (i + 1 == n_chunks) break;
-      const float decay = pw[left - Lc < kLpChunk ? left - Lc : kLpChunk];
-      const unsigned long long decay2 = pk(decay, decay);
+        if (w.whole_start) {
+          // 16 columns x 16 rows at a time: transposed on the way from shared memory
 #pragma unroll 1
-      for (int j = 0; j < DK / 32; ++j) {
-        uint32_t x[32];
-        tmem_ld32(lanes + 32 * j, x);
-        tmem_wait_ld();
-        lp_store_state(s_s, k_s, r, j, x);
+          for (int j = 0; j < DK / 8; ++j) {
+            uint32_t y[4], x[8];
+            ldmatrix_x4_trans(smem_addr(s_s + lp_piece_offset<DK>(j, wq, lane)), y);
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float2 f =
-              upk(mul2(decay2, pk(__uint_as_float(x[e]), __uint_as_float(x[e + 1]))));
-          x[e] = __float_as_uint(f.x);
-          x[e + 1] = __float_as_uint(f.y);
+            for (int e = 0; e < 4; ++e) {
+              x[2 * e] = __float_as_uint(bf16_lo(y[e]) * decay);
+              x[2 * e + 1] = __float_as_uint(bf16_hi(y[e]) * decay);
+            }
+            tmem_st_16x16(lanes + ((16u * (j & 1)) << 16) + 16 * (j >> 1), x);
+          }
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < DK / 32; j += 2) {
+            uint32_t x[2][32];  // two blocks' loads are in flight together
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float4 f =
+                  __ldcg(reinterpret_cast<const float4*>(start + (8 * j + e) * 4 * kLpCols));
+              uint32_t* y = x[e >> 3] + 4 * (e & 7);
+              y[0] = __float_as_uint(f.x);
+              y[1] = __float_as_uint(f.y);
+              y[2] = __float_as_uint(f.z);
+              y[3] = __float_as_uint(f.w);
+            }
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              lp_store_state(s_s, lo_s, r, j + y, x[y]);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                x[y][e] = __float_as_uint(__uint_as_float(x[y][e]) * decay);
+              tmem_st32(lanes + 32 * (j + y), x[y]);
+            }
+          }
         }
-        tmem_st32(lanes + 32 * j, x);
+        if (elected) bulk_wait_read_all();  // the state of the stretch before has left
+        tmem_wait_st();
+        fence_async_smem();
+        tc_fence_before();
+        mbar_arrive(s_ready);
       }
-      tmem_wait_st();
-      fence_async_smem();
-      tc_fence_before();
-      mbar_arrive(s_ready);
-    }
-    // the last state, rounded once, back to the slot through the tile in S_hi's
-    // place (every S^T q has read it)
-    if (final_segment) {
-      if (ok) {
+      for (int i = 0; i < w.n; ++i, ++g) {
+        const int st = g % kStages;
+        const uint32_t use = (g / kStages) & 1;
+        const int left = w.L - i * kLpChunk;
+        const int Lc = left < kLpChunk ? left : kLpChunk;
+        uint8_t* k_s = smem + st * Shape::kStageBytes + kBoxes * kLpBox;
+        const float weight = r < Lc ? decay_power(log_decay, Lc - 1 - r) : 0.0f;
+        // q k^T has read k (and waited for it to land)
+        ok = mbar_wait_abandonable(k_full + 8 * st, use, abort_word, kErrConsumerWait) &&
+             mbar_wait_abandonable(p_raw, g & 1, abort_word, kErrConsumerWait);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        lp_weight_row<kBoxes>(k_s, r, weight);
+        if (Lc < kLpChunk) {  // rows of k and v behind the last token: zeros
+          ok = __all_sync(0xffffffffu, mbar_wait_abandonable(v_full + 8 * st, use, abort_word,
+                                                             kErrConsumerWait));
+          if (!ok) break;
+          if (r >= Lc) {  // v lies behind k
+#pragma unroll 1
+            for (int c = 0; c < 8 * (kBoxes + 2); ++c)
+              *reinterpret_cast<uint4*>(k_s + (c >> 3) * kLpBox + lp_swz(r, c & 7)) =
+                  make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        fence_async_smem();
+        mbar_arrive(k_ready);
+
+        // the sum is done and has read this chunk's k: its stage takes S_lo
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait_abandonable(s_raw, g & 1, abort_word, kErrConsumerWait));
+        if (!ok) break;
+        tc_fence_after();
+        if (i + 1 == w.n) {
+          // every S^T q of the stretch has read S_hi: the next slot may land there
+          if (elected) mbar_arrive(slot_free);
+          ++g;
+          break;
+        }
+        const int next_L = left - Lc < kLpChunk ? left - Lc : kLpChunk;
+        const float decay = decay_power(log_decay, next_L);
+        const unsigned long long decay2 = pk(decay, decay);
 #pragma unroll 1
         for (int j = 0; j < DK / 32; ++j) {
           uint32_t x[32];
           tmem_ld32(lanes + 32 * j, x);
           tmem_wait_ld();
+          lp_store_state(s_s, k_s, r, j, x);
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            *reinterpret_cast<uint16_t*>(s_s + lp_tile_offset<DK>(32 * j + e, r)) =
-                f32_to_bf16_bits(__uint_as_float(x[e]));
+          for (int e = 0; e < 32; e += 2) {
+            const float2 f =
+                upk(mul2(decay2, pk(__uint_as_float(x[e]), __uint_as_float(x[e + 1]))));
+            x[e] = __float_as_uint(f.x);
+            x[e + 1] = __float_as_uint(f.y);
+          }
+          tmem_st32(lanes + 32 * j, x);
+        }
+        tmem_wait_st();
+        fence_async_smem();
+        tc_fence_before();
+        mbar_arrive(s_ready);
+        if (hands && i > 0) pass_on();
+      }
+      if (ok && hands) pass_on();
+      // The stretch's last state: rounded once to the slot, through a tile in the
+      // last chunk's k stage (two-byte stores to the slot itself took 8000 cycles), or
+      // as it is to the next CTA. With segments the next one has its state from the
+      // scan.
+      uint8_t* tile = smem + (g + kStages - 1) % kStages * Shape::kStageBytes + kBoxes * kLpBox;
+      if (ok && (w.whole_end || prm.stream)) {
+        float* hand = prm.starts + 4 * r + static_cast<size_t>(blockIdx.x) * DK * kLpCols;
+        if (w.whole_end) {
+#pragma unroll 1
+          for (int j = 0; j < DK / 8; ++j) {
+            uint32_t x[8], y[4];
+            tmem_ld_16x16(lanes + ((16u * (j & 1)) << 16) + 16 * (j >> 1), x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              y[e] = pack_bf16x2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+            stmatrix_x4_trans(smem_addr(tile + lp_piece_offset<DK>(j, wq, lane)), y);
+          }
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < DK / 16; ++j) {
+            uint32_t x[16];
+            tmem_ld16(lanes + 16 * j, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              __stcg(reinterpret_cast<float4*>(hand + (4 * j + e) * 4 * kLpCols),
+                     make_float4(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1]),
+                                 __uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])));
+          }
         }
       }
       fence_async_smem();
-      if (named_barrier_and(2, 128, ok) && elected) {
-        for (int x = 0; x < cols / 64; ++x)
-          tma_store_3d(&pool_map, col0 + 64 * x, 0, s * p.H_v + h, smem_addr(s_s + x * DK * 128));
+      ok = named_barrier_and(3, 128, ok);
+      hands = ok && prm.stream && !w.whole_end;
+      if (ok && w.whole_end && elected) {
+        for (int x = 0; x < w.cols / 64; ++x)
+          tma_store_3d(&pool_map, w.col0 + 64 * x, 0, w.slot_row,
+                       smem_addr(tile + x * DK * 128));
         bulk_commit_group();
-        bulk_wait_all();
       }
     }
+    if (ok && hands) pass_on();
+    if (elected) bulk_wait_all();
   }
 
   // every warp arrives here: free the tensor memory once no thread can touch it
@@ -808,7 +1093,7 @@ __global__ void __launch_bounds__(kLsThreads, 1)
       const float weight = decay_power(log_decay, (n_chunks - i) * kLpChunk - 1 - r);
       ok = mbar_wait_abandonable(full + 8 * st, (i / kStages) & 1, abort_word, kErrConsumerWait);
       if (!__all_sync(0xffffffffu, ok)) break;
-      lp_weight_row<kBoxes>(smem + st * Shape::kStageBytes, r, weight, true);
+      lp_weight_row<kBoxes>(smem + st * Shape::kStageBytes, r, weight);
       fence_async_smem();
       mbar_arrive(ready + 8 * st);
     }

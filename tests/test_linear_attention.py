@@ -296,6 +296,10 @@ PREFILL = [
     (2, 1, 2, 1700, 128, 192, 3),
     (3, 1, 1, 2900, 64, 320, 3),
     (1, 1, 1, 5000, 128, 64, 1),
+    # more tiles than SMs: equal shares of the chunks, tiles that go on in the next CTA
+    (5, 40, 40, 300, 64, 64, 6),
+    (3, 30, 60, 700, 128, 128, 4),
+    (40, 2, 4, 130, 64, 192, 40),
 ]
 
 
