@@ -538,15 +538,17 @@ __global__ void __launch_bounds__(kLpThreads, 1)
               const uint64_t lo_desc =
                   umma_desc(smem_addr(smem + lo_st * Shape::kStageBytes + kBoxes * kLpBox), 16,
                             1024, kUmmaSwizzle128);
+              // S_lo first: the next chunk's k waits for its place
 #pragma unroll 1
               for (int half = 0; half < 2; ++half) {
-                const uint64_t desc = half ? lo_desc : s_desc;
+                const uint64_t desc = half ? s_desc : lo_desc;
 #pragma unroll 2
                 for (int ks = 0; ks < DK / 16; ++ks) {
                   const uint32_t off = (ks >> 2) * kLpBox + (ks & 3) * 32;
                   umma_bf16_at(tmem + kLpTmemInter, q_k, off, desc, off, id_qk,
                                ks > 0 || half > 0);
                 }
+                if (half == 0) umma_commit(k_free + 8 * lo_st);
               }
             }
             umma_commit(q_free + 8 * st);
@@ -555,7 +557,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
           // A stretch that starts from its slot: the scaled slot is in TMEM, and the
           // state of the stretch before has left the k stage in which S_lo would be.
           if (from_slot && !wait(s_ready, ph)) break;
-          if (leader) umma_commit(k_free + 8 * lo_st);
+          if (from_slot && leader) umma_commit(k_free + 8 * lo_st);
           __syncwarp();
           if (!wait(v_full + 8 * st, use) || !wait(k_ready, ph)) break;
           if (leader) {
