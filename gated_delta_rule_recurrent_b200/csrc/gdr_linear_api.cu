@@ -181,9 +181,13 @@ int launch_linear_decode(const gdr::LinearParams& p, const gdr_host::Device& dev
 
 // How a call's chunks are spread over the SMs.
 //   more tiles than SMs: each SM takes an equal share of all chunks (`stream`);
-//   a third of the SMs' number of tiles or fewer, and 12 chunks or more: each tile
-//     is cut into `segments`, which costs a pass over k and v;
-//   between: a CTA for each tile.
+//   fewer tiles and long prompts: each tile is cut into `segments`;
+//   else: a CTA for each tile.
+// Cutting costs a pass over k and v and two more launches. With c chunks in n
+// segments, D_k = 128, it took about 23 + 3.8 c / n us where one CTA a tile took
+// 12 + 2.5 c (72 tiles of 16 chunks 55 against 52 us and of 32 chunks 85 against
+// 93 us, n = 2; 36 tiles of 8 chunks 27 against 29 us, n = 4; 4 tiles of 64 chunks
+// 27 against 168 us): it is done where the first is less.
 struct PrefillPlan {
   int slices = 1, segments = 1, seg_chunks = 1, grid = 1;
   bool stream = false;
@@ -203,10 +207,12 @@ PrefillPlan plan_prefill(const gdr_dims* d, int sms) {
     s.grid = sms;
     s.states = s.grid * state;
     s.workspace = s.states + s.grid * 4;
-  } else if (3 * tiles <= sms && chunks >= 12) {
-    int n = static_cast<int>(sms / tiles);
-    if (n > chunks / 4) n = chunks / 4;
-    s.seg_chunks = (chunks - 1) / n + 1;
+    return s;
+  }
+  long long n = sms / tiles;
+  if (n > chunks / 2) n = chunks / 2;
+  if (n >= 2 && chunks * (25 * n - 38) > 110 * n) {
+    s.seg_chunks = static_cast<int>((chunks - 1) / n + 1);
     s.segments = (chunks - 1) / s.seg_chunks + 1;
     s.grid = static_cast<int>(tiles) * s.segments;
     s.states = s.workspace = tiles * s.segments * state;

@@ -300,6 +300,9 @@ PREFILL = [
     (5, 40, 40, 300, 64, 64, 6),
     (3, 30, 60, 700, 128, 128, 4),
     (40, 2, 4, 130, 64, 192, 40),
+    (9, 10, 20, 3, 128, 64, 9),
+    # and more items than a CTA counts
+    (300, 1, 1, 5, 64, 64, 300),
 ]
 
 
@@ -318,6 +321,38 @@ def test_prefill_lengths_and_slots_out_of_range(Dk):
     x = draw(9, 1, 2, T, Dk, 128, 7, seed=8, lengths=[T, 0, -3, T + 5, 1, 128, 129, 256, 200],
              indices=[0, 1, 2, 3, 4, 5, 6, -1, 7])
     run_and_check(x, "prefill")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(2, 1, 2, 200, 64, 128, 2), (4, 40, 40, 140, 128, 64, 4),
+                                   (1, 1, 1, 3000, 64, 64, 1)], ids=str)
+def test_prefill_of_nothing(shape):
+    """Every item empty or without a slot: zeros out, no slot touched."""
+    x = draw(*shape, seed=16, lengths=[0] * shape[0])
+    run_and_check(x, "prefill")
+    x = draw(*shape, seed=16, lengths=[shape[3]] * shape[0], indices=[shape[6]] * shape[0])
+    run_and_check(x, "prefill")
+
+
+@pytest.mark.gpu
+def test_two_prefills_on_two_streams_do_not_share_a_workspace():
+    """Calls that need a workspace, queued side by side: each has its own."""
+    x = draw(1, 1, 2, 2500, 64, 64, 1, seed=17, device="cuda")
+    want = call(dict(x, state_pool=x["state_pool"].clone()), "prefill")
+    y = draw(1, 1, 2, 2500, 64, 64, 1, seed=18, device="cuda")
+    want_y = call(dict(y, state_pool=y["state_pool"].clone()), "prefill")
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(4):
+        for z, stream in zip((x, y), streams):
+            with torch.cuda.stream(stream):
+                got.append(call(dict(z, state_pool=z["state_pool"].clone()), "prefill"))
+    torch.cuda.synchronize()
+    for k, (out, pool) in enumerate(got):
+        w = (want, want_y)[k % 2]
+        assert torch.equal(out.view(torch.int16), w[0].view(torch.int16))
+        assert torch.equal(pool.view(torch.int16), w[1].view(torch.int16))
 
 
 @pytest.mark.gpu
@@ -343,10 +378,14 @@ def test_prefill_in_two_calls_and_then_decode(Dk):
     assert np.linalg.norm(out - ref[0]) <= 6e-3 * np.linalg.norm(ref[0])
 
 
+# the last three: a CTA for each tile, tiles cut into segments, equal shares
+REPEATS = [("decode", (2, 2, 2, 1, 64, 128, 3)), ("decode", (2, 2, 2, 5, 128, 64, 3)),
+           ("prefill", (2, 2, 2, 200, 128, 192, 3)), ("prefill", (1, 1, 2, 2500, 64, 64, 1)),
+           ("prefill", (4, 20, 40, 500, 128, 128, 4))]
+
+
 @pytest.mark.gpu
-@pytest.mark.parametrize("op,shape", [("decode", (2, 2, 2, 1, 64, 128, 3)),
-                                      ("decode", (2, 2, 2, 5, 128, 64, 3)),
-                                      ("prefill", (2, 2, 2, 200, 128, 192, 3))])
+@pytest.mark.parametrize("op,shape", REPEATS, ids=str)
 def test_results_repeat_and_do_not_depend_on_the_stream(op, shape):
     x = draw(*shape, seed=12, device="cuda")
     pools, outs = [], []
@@ -368,9 +407,7 @@ def test_results_repeat_and_do_not_depend_on_the_stream(op, shape):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("op,shape", [("decode", (2, 2, 2, 1, 64, 128, 3)),
-                                      ("decode", (2, 2, 2, 5, 128, 64, 3)),
-                                      ("prefill", (2, 2, 2, 200, 128, 192, 3))])
+@pytest.mark.parametrize("op,shape", REPEATS, ids=str)
 def test_graph_replay(op, shape):
     x = draw(*shape, seed=13, device="cuda")
     start = x["state_pool"].clone()
@@ -415,7 +452,9 @@ GUARD = 4096
 @pytest.mark.parametrize("op,shape", [("decode", (2, 2, 4, 1, 64, 192, 4)),
                                       ("decode", (2, 2, 4, 6, 128, 192, 4)),
                                       ("prefill", (2, 2, 4, 150, 128, 192, 4)),
-                                      ("prefill", (2, 2, 4, 150, 64, 64, 4))])
+                                      ("prefill", (2, 2, 4, 150, 64, 64, 4)),
+                                      ("prefill", (1, 1, 2, 1700, 64, 64, 2)),
+                                      ("prefill", (4, 20, 40, 200, 64, 64, 5))])
 def test_nothing_is_written_outside(op, shape):
     """Every tensor sits between guard bands; bands and inputs keep their bits."""
     x = draw(*shape, seed=15)
@@ -473,3 +512,83 @@ def test_empty_batch_queues_nothing():
         out, _ = call(x, op)
         assert out.shape == (0, 1, 2, 64)
         assert gdr.last_launch()["kernel"] == "none"
+
+
+# ------------------------------------------------------------------ a wait that runs out
+
+
+@pytest.fixture(scope="module")
+def hooks():
+    """The test build, in which a producer can hold a block's loads back and the budget of
+    the waits is short."""
+    from gated_delta_rule_recurrent_b200 import binding, build
+
+    L = ctypes.CDLL(build.ensure_built(test_hooks=True))
+    for name in ("gdr_linear_attention_decode", "gdr_linear_attention_prefill",
+                 "gdr_linear_attention_prefill_workspace", "gdr_device_error"):
+        getattr(L, name).argtypes = getattr(binding.lib(), name).argtypes
+    L.gdrtest_set_hooks.argtypes = [ctypes.c_longlong, ctypes.c_int]
+    yield L
+    assert L.gdrtest_set_hooks(0, -1) == 0
+
+
+def _hooked_call(L, x, op):
+    from gated_delta_rule_recurrent_b200 import binding
+
+    P = binding._ptr
+    B, Hq, T, Dk = x["query"].shape
+    Hv, Dv = x["value"].shape[1], x["value"].shape[3]
+    d = binding.Dims(B, T, Hq, Hv, Dk, Dv, x["state_pool"].shape[0], 0)
+    out = torch.zeros_like(x["value"])
+    args = [ctypes.byref(d), *(P(x[n]) for n in ("query", "key", "value", "log_decay",
+                                                  "state_pool", "lengths", "indices"))]
+    stream = torch.cuda.current_stream().cuda_stream
+    if op == "decode":
+        rc = L.gdr_linear_attention_decode(*args, None, x["scale"], P(out), stream)
+    else:
+        need = ctypes.c_int64(0)
+        assert L.gdr_linear_attention_prefill_workspace(ctypes.byref(d), ctypes.byref(need)) == 0
+        work = torch.empty(max(need.value, 16), dtype=torch.uint8, device="cuda")
+        rc = L.gdr_linear_attention_prefill(*args, x["scale"], P(out), P(work), need.value,
+                                            stream)
+    assert rc == 0
+    torch.cuda.synchronize()
+    flags = ctypes.c_uint32(0)
+    assert L.gdr_device_error(ctypes.byref(flags), 1) == 0
+    return out, flags.value
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("op,shape,held", [
+    ("decode", (2, 1, 3, 1, 128, 64, 2), 4),
+    ("decode", (2, 1, 3, 8, 64, 64, 2), 1),
+    ("prefill", (2, 1, 3, 300, 128, 128, 2), 4),     # a CTA for each tile
+    ("prefill", (1, 1, 1, 2000, 64, 64, 1), 3),      # segments
+    ("prefill", (4, 20, 40, 300, 64, 64, 4), 70),    # equal shares, states handed on
+])
+def test_held_loads_time_out_cleanly(hooks, op, shape, held):
+    """The call ends, says so in the error word, leaves each slot old or right, and the next
+    call is right."""
+    x = draw(*shape, seed=19, lengths=[shape[3]] * shape[0])
+    ref, mag = oracle(x), oracle(x, absolute=True)
+    fresh = lambda: {k: v.cuda() if isinstance(v, torch.Tensor) else v  # noqa: E731
+                     for k, v in x.items()}
+    xd = fresh()
+    assert _hooked_call(hooks, xd, op)[1] == 0
+    xd = fresh()
+    assert hooks.gdrtest_set_hooks(4_000_000, held) == 0
+    _, word = _hooked_call(hooks, xd, op)
+    assert hooks.gdrtest_set_hooks(0, -1) == 0
+    assert word & 3 and not word & 4, word
+    now, was = f64(xd["state_pool"]), f64(x["state_pool"])
+    right = np.abs(now - ref[1]) <= U * np.abs(ref[1]) * 1.01 + (U + 2.0 ** -12) * mag[1]
+    assert np.all(right | (now == was))
+    if op == "decode" or shape[0] == 2:  # block `held` is value head `held` of all items
+        b, h = divmod(held, shape[2])
+        slot = int(x["indices"][b])
+        assert np.array_equal(now[slot, h], was[slot, h])
+        assert right.reshape(*right.shape[:2], -1).all(-1).sum() >= shape[0] * shape[2] - 1
+    xd = fresh()
+    out, word = _hooked_call(hooks, xd, op)
+    assert word == 0
+    check(x, op, (out, xd["state_pool"]), ref, mag, x["state_pool"])
