@@ -17,8 +17,9 @@
 //            P V with P read from TMEM;
 //   P        P out of TMEM, times lambda^{i-j}, masked, back as bf16 over
 //            itself;
-//   out      (S^T q) lambda^{i+1} + P V, scaled, to bf16 in the chunk's v stage
-//            (both products have read v by then), TMA store;
+//   out      (S^T q) lambda^{i+1} to where P V is then added to it; their sum,
+//            scaled, to bf16 in the chunk's v stage (both products have read v by
+//            then), TMA store;
 //   state    k in place times lambda^{C-1-j}; then S out of TMEM to a pair of
 //            bf16 tiles (S_hi, and S_lo = S - S_hi, which takes the place of
 //            the chunk's k) for the next chunk's S^T q, and back scaled by
@@ -67,7 +68,7 @@ constexpr int kLpRegsFew = 56, kLpRegsMany = 152;  // 128 * 56 + 384 * 152 = 655
 constexpr int kLpBox = kLpChunk * 128;     // bytes of 128 rows x 64 bf16
 constexpr int kLpTmemCols = 512;
 constexpr int kLpTmemP = 0, kLpTmemInter = 128, kLpTmemIntra = 256, kLpTmemState = 384;
-constexpr int kLpBars = 10;                // besides six per stage and two per work entry
+constexpr int kLpBars = 11;                // besides six per stage and two per work entry
 constexpr int kLpWorks = 4;                // work entries in the ring
 constexpr int kLpReaders = 14;             // warps that read them
 
@@ -79,9 +80,13 @@ struct LpShape {
   static constexpr int kStateOff = kStages * kStageBytes;        // bf16 S^T, [128 j][DK]
   static constexpr int kBarOff = kStateOff + kBoxes * kLpBox;
   static constexpr int kPowOff = kBarOff + 8 * (6 * kStages + kLpBars + 2 * kLpWorks) + 16;
-  static constexpr int kWorkOff = kPowOff + 4 * 32;
+  static constexpr int kWorkOff = (kPowOff + 4 * 32 + 15) / 16 * 16;
   static constexpr int kLenOff = kWorkOff + 64 * kLpWorks;
   static constexpr int kSmem = 1024 + kLenOff + 4 * (kLpItems + 1);
+  static_assert(kStageBytes % 1024 == 0 && kStateOff % 1024 == 0 && kBarOff % 8 == 0 &&
+                    kPowOff % 4 == 0 && kWorkOff % 16 == 0 && kLenOff % 4 == 0,
+                "alignment of what lies there");
+  static_assert(kSmem <= 232448, "shared memory of a block");
 };
 
 struct LinearPrefillParams {
@@ -309,8 +314,8 @@ __global__ void __launch_bounds__(kLpThreads, 1)
   const uint32_t v_free = bar0 + 40 * kStages;     // + 8 st: the output has left the v stage
   const uint32_t bar1 = bar0 + 48 * kStages;
   const uint32_t p_raw = bar1, p_ready = bar1 + 8, k_ready = bar1 + 16, s_ready = bar1 + 24,
-                 s_raw = bar1 + 32, o_raw = bar1 + 40, o_free = bar1 + 48, drained = bar1 + 56,
-                 slot_full = bar1 + 64, slot_free = bar1 + 72;
+                 s_raw = bar1 + 32, o_raw = bar1 + 40, i_raw = bar1 + 48, i_ready = bar1 + 56,
+                 drained = bar1 + 64, slot_full = bar1 + 72, slot_free = bar1 + 80;
   const uint32_t work_full = bar1 + 8 * kLpBars;     // + 8 e: entry e of the ring written
   const uint32_t work_free = work_full + 8 * kLpWorks;  // + 8 e: read by everyone
   uint32_t* tmem_slot =
@@ -406,7 +411,8 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     mbar_init(s_ready, 128);
     mbar_init(s_raw, 1);
     mbar_init(o_raw, 1);
-    mbar_init(o_free, 128);
+    mbar_init(i_raw, 1);
+    mbar_init(i_ready, 128);
     mbar_init(drained, 1);
     mbar_init(slot_full, 1);
     mbar_init(slot_free, 1);
@@ -521,7 +527,6 @@ __global__ void __launch_bounds__(kLpThreads, 1)
           __syncwarp();
           const bool from_slot = i == 0 && w.whole_start;
           if (!wait(from_slot ? slot_full : s_ready, from_slot ? slots & 1 : ph)) break;
-          if (g > 0 && !wait(o_free, ph ^ 1)) break;
           const int lo_st = (g + kStages - 1) % kStages;  // the k stage that holds S_lo
           if (from_slot) ++slots;
           if (leader) {
@@ -551,6 +556,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                 if (half == 0) umma_commit(k_free + 8 * lo_st);
               }
             }
+            umma_commit(i_raw);
             umma_commit(q_free + 8 * st);
           }
           __syncwarp();
@@ -571,13 +577,13 @@ __global__ void __launch_bounds__(kLpThreads, 1)
           // switched off, so that fetching them (3500 cycles, cold) falls into the wait.
           bool p_ok = true;
           for (int run = g > 0; run < 2; ++run) {
-            if (run) p_ok = wait(p_ready, ph);
+            if (run) p_ok = wait(p_ready, ph) && wait(i_ready, ph);
             if (!p_ok) break;
             if (leader) {
 #pragma unroll 2
               for (int ks = 0; ks < kLpChunk / 16; ++ks)
                 umma_bf16_ts_at(tmem + kLpTmemIntra, tmem + kLpTmemP + 8 * ks, v_mn, ks * 2048,
-                                id_pv, ks > 0, run != 0);
+                                id_pv, true, run != 0);
             }
             __syncwarp();
           }
@@ -701,24 +707,53 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * wq) << 16);
     const unsigned long long scale2 = pk(p.scale, p.scale);
     const bool elected = t == 0;
+    int leaving = -1;  // the v stage that an output is leaving
     bool ok = true;
     int g = 0;
     while (ok && next_work()) {
-      const float inter = decay_power(w.log_decay, t + 1) * p.scale;
+      const float inter = decay_power(w.log_decay, t + 1);
       const unsigned long long inter2 = pk(inter, inter);
       for (int i = 0; i < w.n; ++i, ++g) {
         const int st = g % kStages;
         const uint32_t valid = t < w.L - i * kLpChunk ? 0xffffffffu : 0u;  // padding: +0.0
         uint8_t* o_s = smem + st * Shape::kStageBytes + 2 * kBoxes * kLpBox;
+        // S^T q times lambda^{t+1} to where P V will be added to it
         ok = __all_sync(0xffffffffu,
-                        mbar_wait_abandonable(o_raw, g & 1, abort_word, kErrConsumerWait));
+                        mbar_wait_abandonable(i_raw, g & 1, abort_word, kErrConsumerWait));
         if (ok) {
           tc_fence_after();
 #pragma unroll 1
           for (int j = 0; j < 4; ++j) {
-            uint32_t x[32], z[32];
+            uint32_t x[32];
             tmem_ld32(lanes + kLpTmemInter + 32 * j, x);
-            tmem_ld32(lanes + kLpTmemIntra + 32 * j, z);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float2 f =
+                  upk(mul2(pk(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), inter2));
+              x[e] = __float_as_uint(f.x);
+              x[e + 1] = __float_as_uint(f.y);
+            }
+            tmem_st32(lanes + kLpTmemIntra + 32 * j, x);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(i_ready);
+        }
+        // the output before has left its v stage by now
+        if (elected && leaving >= 0) {
+          bulk_wait_read_all();
+          mbar_arrive(v_free + 8 * leaving);
+          leaving = -1;
+        }
+        ok = ok && mbar_wait_abandonable(o_raw, g & 1, abort_word, kErrConsumerWait);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int j = 0; j < 4; ++j) {
+            uint32_t x[32];
+            tmem_ld32(lanes + kLpTmemIntra + 32 * j, x);
             tmem_wait_ld();
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -726,9 +761,8 @@ __global__ void __launch_bounds__(kLpThreads, 1)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const int k = 8 * c + 2 * e;
-                const float2 f = upk(
-                    fma2(pk(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), inter2,
-                         mul2(pk(__uint_as_float(z[k]), __uint_as_float(z[k + 1])), scale2)));
+                const float2 f =
+                    upk(mul2(pk(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), scale2));
                 y[e] = pack_bf16x2(f.x, f.y) & valid;
               }
               *reinterpret_cast<uint4*>(o_s + (j >> 1) * kLpBox + lp_swz(t, 4 * (j & 1) + c)) =
@@ -736,7 +770,6 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             }
           }
           tc_fence_before();
-          mbar_arrive(o_free);
         }
         fence_async_smem();
         ok = named_barrier_and(2, 128, ok);
@@ -746,8 +779,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
             tma_store_3d(&o_map, w.col0 + 64 * x, (w.c0 + i) * kLpChunk, w.bh,
                          smem_addr(o_s + x * kLpBox));
           bulk_commit_group();
-          bulk_wait_read_all();
-          mbar_arrive(v_free + 8 * st);
+          leaving = st;
         }
       }
     }
