@@ -387,16 +387,9 @@ def linear_attention_gate(a: torch.Tensor, dt_bias: torch.Tensor, decay_scale: t
     return decay, beta
 
 
-def _is(t, dtype: torch.dtype, shape: tuple, index: int) -> bool:
-    """Whether t is a contiguous tensor of that type and shape on CUDA device ``index``: the
-    conditions of ``_need``, which names the one that fails."""
-    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.get_device() == index and t.is_contiguous())
-
-
 def _call(index: int, fn, *args) -> None:
     """The library's ``fn(*args)`` with CUDA device ``index`` as the current one."""
-    if torch.cuda.current_device() == index:
+    if _device() == index:
         rc = fn(*args)
     else:
         with torch.cuda.device(index):
@@ -405,6 +398,9 @@ def _call(index: int, fn, *args) -> None:
         _check(rc)
 
 
+# The current device, without the check for initialisation around it (a CUDA
+# tensor is there) where this torch has the function.
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 # The handle of a device's current stream, without the Stream object around it
 # where this torch has the function.
 _stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -413,36 +409,55 @@ _stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 def _linear_args(query, key, value, log_decay, state_pool, actual_seq_lengths,
                  ssm_state_indices, num_accepted_tokens, out):
-    if not isinstance(query, torch.Tensor) or query.dim() != 4:
-        raise RuntimeError("query must be a 4-D tensor [B, H_qk, T, D_k]")
-    if not query.is_cuda:
-        raise RuntimeError("all tensors must be on a CUDA device")
-    if not isinstance(value, torch.Tensor) or value.dim() != 4:
-        raise RuntimeError("value must be a 4-D tensor [B, H_v, T, D_v]")
-    if not isinstance(state_pool, torch.Tensor) or state_pool.dim() != 4:
-        raise RuntimeError("state_pool must be a 4-D tensor [pool, H_v, D_k, D_v]")
-    index = query.get_device()
-    B, H_qk, T, D_k = qk = tuple(query.shape)
-    vo = value.shape
-    H_v, D_v = vo[1], vo[3]
-    P = state_pool.shape[0]
-    bf16, i32 = torch.bfloat16, torch.int32
-    wanted = ((query, "query", bf16, qk), (key, "key", bf16, qk),
-              (value, "value", bf16, (B, H_v, T, D_v)),
-              (log_decay, "log_decay", torch.float32, (H_v,)),
-              (state_pool, "state_pool", bf16, (P, H_v, D_k, D_v)),
-              (actual_seq_lengths, "actual_seq_lengths", i32, (B,)),
-              (ssm_state_indices, "ssm_state_indices", i32, (B,)))
-    for t, name, dtype, shape in wanted:
-        if not _is(t, dtype, shape, index):
+    """(device index, Dims, out) of a linear-attention call, its tensors checked."""
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    try:
+        index = query.get_device()
+        B, H_qk, T, D_k = qk = query.shape
+        _, H_v, _, D_v = value.shape
+        P = state_pool.shape[0]
+        # every condition of the list below, in one go: a call costs a few
+        # microseconds of the host, and a step of one sequence no more of the GPU
+        good = (
+            index >= 0 and query.dtype is bf16 and key.dtype is bf16 and value.dtype is bf16
+            and state_pool.dtype is bf16 and log_decay.dtype is f32
+            and actual_seq_lengths.dtype is i32 and ssm_state_indices.dtype is i32
+            and key.shape == qk and value.shape == (B, H_v, T, D_v)
+            and state_pool.shape == (P, H_v, D_k, D_v) and log_decay.shape == (H_v,)
+            and actual_seq_lengths.shape == (B,) and ssm_state_indices.shape == (B,)
+            and key.get_device() == index and value.get_device() == index
+            and state_pool.get_device() == index and log_decay.get_device() == index
+            and actual_seq_lengths.get_device() == index
+            and ssm_state_indices.get_device() == index
+            and query.is_contiguous() and key.is_contiguous() and value.is_contiguous()
+            and state_pool.is_contiguous() and log_decay.is_contiguous()
+            and actual_seq_lengths.is_contiguous() and ssm_state_indices.is_contiguous())
+    except (AttributeError, ValueError, IndexError):
+        good = False
+    if not good:  # which one
+        for t, name, dims in ((query, "query", "[B, H_qk, T, D_k]"),
+                              (value, "value", "[B, H_v, T, D_v]"),
+                              (state_pool, "state_pool", "[pool, H_v, D_k, D_v]")):
+            if not isinstance(t, torch.Tensor) or t.dim() != 4:
+                raise RuntimeError(f"{name} must be a 4-D tensor {dims}")
+        if not query.is_cuda:
+            raise RuntimeError("all tensors must be on a CUDA device")
+        B, H_qk, T, D_k = qk = tuple(query.shape)
+        H_v, D_v, P = value.shape[1], value.shape[3], state_pool.shape[0]
+        for t, name, dtype, shape in (
+                (query, "query", bf16, qk), (key, "key", bf16, qk),
+                (value, "value", bf16, (B, H_v, T, D_v)), (log_decay, "log_decay", f32, (H_v,)),
+                (state_pool, "state_pool", bf16, (P, H_v, D_k, D_v)),
+                (actual_seq_lengths, "actual_seq_lengths", i32, (B,)),
+                (ssm_state_indices, "ssm_state_indices", i32, (B,))):
             _need(t, name, dtype, shape, query.device)
-    if num_accepted_tokens is not None and not _is(num_accepted_tokens, i32, (B,), index):
+    if num_accepted_tokens is not None:
         _need(num_accepted_tokens, "num_accepted_tokens", i32, (B,), query.device)
     if out is None:
         out = torch.empty_like(value)
-    elif not _is(out, bf16, vo, index):
-        _need(out, "out", bf16, vo, query.device)
-    return index, Dims(B, T, H_qk, H_v, D_k, D_v, P, 0), out
+    else:
+        _need(out, "out", bf16, value.shape, query.device)
+    return index, Dims(B, T, H_qk, H_v, D_k, D_v, P), out
 
 
 def linear_attention_decode(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
@@ -506,30 +521,49 @@ _CACHE_GROUP = 64
 
 
 def _cache_args(state_pool, ssm_state_indices, cache, scales, cache_indices):
-    for t, name in ((state_pool, "state_pool"), (cache, "cache")):
-        if not isinstance(t, torch.Tensor) or t.dim() != 4:
-            raise RuntimeError(f"{name} must be a 4-D tensor ([pool or entries, H_v, rows, "
-                               "columns])")
-    if not state_pool.is_cuda:
-        raise RuntimeError("all tensors must be on a CUDA device")
-    index = state_pool.get_device()
-    P, H, R, C = slots = tuple(state_pool.shape)
-    N = cache.shape[0]
-    kind = _CACHE_TYPES.get(cache.dtype)
-    if kind is None:
-        raise RuntimeError(f"cache must be int8 or float8_e4m3fn, got {cache.dtype}")
-    if C % _CACHE_GROUP != 0:
-        raise RuntimeError("state_pool's last axis must be a multiple of 64")
-    if not isinstance(ssm_state_indices, torch.Tensor) or ssm_state_indices.dim() != 1:
-        raise RuntimeError("ssm_state_indices must be a 1-D tensor")
-    n = ssm_state_indices.shape[0]
-    for t, name, dtype, shape in (
-            (state_pool, "state_pool", torch.bfloat16, slots),
-            (cache, "cache", cache.dtype, (N, H, R, C)),
-            (scales, "scales", torch.float32, (N, H, R, C // _CACHE_GROUP)),
-            (ssm_state_indices, "ssm_state_indices", torch.int32, (n,)),
-            (cache_indices, "cache_indices", torch.int32, (n,))):
-        if not _is(t, dtype, shape, index):
+    """(device index, slots, entries, pairs, values of a slot, cache type) of a cache call,
+    its tensors checked."""
+    i32 = torch.int32
+    try:
+        index = state_pool.get_device()
+        P, H, R, C = state_pool.shape
+        N = cache.shape[0]
+        n, = ssm_state_indices.shape
+        kind = _CACHE_TYPES.get(cache.dtype)
+        good = (  # in one go, as in _linear_args
+            index >= 0 and kind is not None and C % _CACHE_GROUP == 0
+            and state_pool.dtype is torch.bfloat16 and scales.dtype is torch.float32
+            and ssm_state_indices.dtype is i32 and cache_indices.dtype is i32
+            and cache.shape == (N, H, R, C) and scales.shape == (N, H, R, C // _CACHE_GROUP)
+            and cache_indices.shape == (n,) and cache.get_device() == index
+            and scales.get_device() == index and ssm_state_indices.get_device() == index
+            and cache_indices.get_device() == index and state_pool.is_contiguous()
+            and cache.is_contiguous() and scales.is_contiguous()
+            and ssm_state_indices.is_contiguous() and cache_indices.is_contiguous())
+    except (AttributeError, ValueError, IndexError):
+        good = False
+    if not good:  # which one
+        for t, name in ((state_pool, "state_pool"), (cache, "cache")):
+            if not isinstance(t, torch.Tensor) or t.dim() != 4:
+                raise RuntimeError(f"{name} must be a 4-D tensor ([pool or entries, H_v, rows, "
+                                   "columns])")
+        if not state_pool.is_cuda:
+            raise RuntimeError("all tensors must be on a CUDA device")
+        if cache.dtype not in _CACHE_TYPES:
+            raise RuntimeError(f"cache must be int8 or float8_e4m3fn, got {cache.dtype}")
+        P, H, R, C = state_pool.shape
+        N = cache.shape[0]
+        if C % _CACHE_GROUP != 0:
+            raise RuntimeError("state_pool's last axis must be a multiple of 64")
+        if not isinstance(ssm_state_indices, torch.Tensor) or ssm_state_indices.dim() != 1:
+            raise RuntimeError("ssm_state_indices must be a 1-D tensor")
+        n = ssm_state_indices.shape[0]
+        for t, name, dtype, shape in (
+                (state_pool, "state_pool", torch.bfloat16, (P, H, R, C)),
+                (cache, "cache", cache.dtype, (N, H, R, C)),
+                (scales, "scales", torch.float32, (N, H, R, C // _CACHE_GROUP)),
+                (ssm_state_indices, "ssm_state_indices", i32, (n,)),
+                (cache_indices, "cache_indices", i32, (n,))):
             _need(t, name, dtype, shape, state_pool.device)
     return index, P, N, n, H * R * C, kind
 
