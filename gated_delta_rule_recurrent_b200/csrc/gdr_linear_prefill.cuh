@@ -635,10 +635,18 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         from = from > first ? from : first;
         to = to < last ? to : last;
       }
+      // a warp writes 512 bytes a store, four stores a turn
       const int rows = 32 >> sh;
-      uint16_t* at = p.out + static_cast<size_t>(bh) * p.T * p.D_v + col0 +
-                     (from + (lane >> sh)) * p.D_v + (lane & ((1 << sh) - 1)) * 8;
-      for (int64_t i = from + (lane >> sh); i < to; i += rows, at += static_cast<size_t>(rows) * p.D_v)
+      const size_t step_rows = static_cast<size_t>(rows) * p.D_v;
+      int64_t i = from + (lane >> sh);
+      uint16_t* at = p.out + (static_cast<size_t>(bh) * p.T + i) * p.D_v + col0 +
+                     (lane & ((1 << sh) - 1)) * 8;
+      for (; i + 3 * rows < to; i += 4 * rows, at += 4 * step_rows) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<uint4*>(at + e * step_rows) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      for (; i < to; i += rows, at += step_rows)
         *reinterpret_cast<uint4*>(at) = make_uint4(0u, 0u, 0u, 0u);
     }
   } else if (warp < 8) {

@@ -335,11 +335,13 @@ def test_prefill_of_nothing(shape):
 
 
 @pytest.mark.gpu
-def test_two_prefills_on_two_streams_do_not_share_a_workspace():
+@pytest.mark.parametrize("shape", [(1, 1, 2, 2500, 64, 64, 1), (4, 20, 40, 300, 64, 64, 4)],
+                         ids=str)
+def test_two_prefills_on_two_streams_do_not_share_a_workspace(shape):
     """Calls that need a workspace, queued side by side: each has its own."""
-    x = draw(1, 1, 2, 2500, 64, 64, 1, seed=17, device="cuda")
+    x = draw(*shape, seed=17, device="cuda")
     want = call(dict(x, state_pool=x["state_pool"].clone()), "prefill")
-    y = draw(1, 1, 2, 2500, 64, 64, 1, seed=18, device="cuda")
+    y = draw(*shape, seed=18, device="cuda")
     want_y = call(dict(y, state_pool=y["state_pool"].clone()), "prefill")
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
@@ -353,6 +355,14 @@ def test_two_prefills_on_two_streams_do_not_share_a_workspace():
         w = (want, want_y)[k % 2]
         assert torch.equal(out.view(torch.int16), w[0].view(torch.int16))
         assert torch.equal(pool.view(torch.int16), w[1].view(torch.int16))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,H,T", [(1, 2, 9000), (8, 20, 1000), (1, 3, 1000)])
+def test_prefill_of_short_items_in_a_long_call(B, H, T):
+    """Most of the output is padding, which every mode writes as zeros."""
+    x = draw(B, H, H, T, 64, 192, B, seed=20, lengths=[3 + 20 * b for b in range(B)])
+    run_and_check(x, "prefill")
 
 
 @pytest.mark.gpu
