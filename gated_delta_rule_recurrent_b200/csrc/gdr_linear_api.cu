@@ -180,7 +180,8 @@ int launch_linear_decode(const gdr::LinearParams& p, const gdr_host::Device& dev
 // ---------------------------------------------------------------- prefill
 
 // How a call's chunks are spread over the SMs.
-//   more tiles than SMs: each SM takes an equal share of all chunks (`stream`);
+//   more tiles than SMs: each SM takes an equal share of all chunks (`stream`), in
+//     teams of tiles that read the same q and k;
 //   fewer tiles and long prompts: each tile is cut into `segments`;
 //   else: a CTA for each tile.
 // Cutting costs a pass over k and v and two more launches. With c chunks in n
@@ -189,7 +190,7 @@ int launch_linear_decode(const gdr::LinearParams& p, const gdr_host::Device& dev
 // 93 us, n = 2; 36 tiles of 8 chunks 27 against 29 us, n = 4; 4 tiles of 64 chunks
 // 27 against 168 us): it is done where the first is less.
 struct PrefillPlan {
-  int slices = 1, segments = 1, seg_chunks = 1, grid = 1;
+  int slices = 1, segments = 1, seg_chunks = 1, team = 1, grid = 1;
   bool stream = false;
   int64_t states = 0;     // bytes of states in the workspace
   int64_t workspace = 0;  // and of all of it
@@ -204,7 +205,12 @@ PrefillPlan plan_prefill(const gdr_dims* d, int sms) {
   s.grid = static_cast<int>(tiles);
   if (tiles > sms && d->B <= gdr::kLpItems && tiles * chunks < kMaxGrid) {
     s.stream = true;
-    s.grid = sms;
+    // tiles that read the same q and k run side by side, up to 8 of them, as long
+    // as teams of that many leave no more than 1 in 16 SMs idle
+    const int sharing = d->H_v / d->H_qk * s.slices;
+    for (int m = 2; m <= 8; ++m)
+      if (sharing % m == 0 && 16 * (sms % m) <= sms) s.team = m;
+    s.grid = sms / s.team * s.team;
     s.states = s.grid * state;
     s.workspace = s.states + s.grid * 4;
     return s;
@@ -270,6 +276,7 @@ int launch_linear_prefill(const gdr::LinearParams& p, const PrefillPlan& plan, u
   prm.p = p;
   prm.slices = plan.slices;
   prm.stream = plan.stream;
+  prm.team = plan.team;
   prm.segments = plan.segments;
   prm.seg_chunks = plan.seg_chunks;
   prm.starts = reinterpret_cast<float*>(workspace);

@@ -92,14 +92,15 @@ struct LpShape {
 struct LinearPrefillParams {
   LinearParams p;
   int slices;      // ceil(D_v / 128)
-  int stream;      // nonzero: every CTA takes an equal share of all tiles' chunks
+  int stream;      // nonzero: every team of CTAs takes an equal share of all chunks
+  int team;        // CTAs of a team: that many consecutive tiles read the same q and k
   int segments;    // of a tile (1: not cut), with stream = 0
   int seg_chunks;  // chunks of a segment
   // States between CTAs, [D_k / 4][128 columns][4 rows] each (four rows of a column
   // are one 16-byte access, coalesced over the columns). With segments
   // [tiles][segments]: entry g >= 1 is the sum of segment g - 1 after the first
   // pass, the first state of segment g after the scan. With stream [CTAs]: what CTA
-  // c hands to CTA c + 1, which may read it once flags[c] is set.
+  // c hands to CTA c + team, which may read it once flags[c] is set.
   float* starts;
   int* flags;
 };
@@ -121,10 +122,12 @@ static_assert(sizeof(LpWork) <= 64, "an entry of the ring");
 // it for itself cost 4000 cycles a stretch, most of them for fetching code that
 // runs once a stretch).
 //   stream = 0: one, segment blockIdx.x % segments of tile blockIdx.x / segments.
-//   stream = 1: the CTA's share [lo, hi) of all chunks in tile order, last tile
-//     first: a tile that goes on in the next CTA's share comes first, so that its
-//     state is handed over early, and one that began in the share before comes
-//     last, when that state has long been there.
+//   stream = 1: `team` consecutive tiles, which read the same q and k, are a unit,
+//     and a team of as many CTAs takes a share [lo, hi) of the chunks in the order
+//     of the units, each CTA its tile of a unit: they run side by side, and q and k
+//     come from HBM once for all of them. The last unit comes first: one that goes
+//     on in the next team's share hands its states over early, and one that began
+//     in the share before comes last, when those have long been there.
 struct LpWalk {
   const LinearPrefillParams& prm;
   const int* before;  // stream: chunks of all items ahead of item b
@@ -133,9 +136,9 @@ struct LpWalk {
     w.n = 0;
     if (hi <= lo) return;
     const LinearParams& p = prm.p;
-    const int per_item = p.H_v * prm.slices;
     int tile, chunks;
     if (prm.stream) {
+      const int per_item = p.H_v * prm.slices / prm.team;
       int b0 = 0, b1 = p.B - 1;  // the item of chunk hi - 1
       while (b0 < b1) {
         const int m = (b0 + b1 + 1) >> 1;
@@ -148,7 +151,7 @@ struct LpWalk {
       chunks = (before[b0 + 1] - before[b0]) / per_item;
       const int in_item = (hi - 1 - before[b0]) / chunks;
       const int first = before[b0] + in_item * chunks;
-      tile = b0 * per_item + in_item;
+      tile = (b0 * per_item + in_item) * prm.team + static_cast<int>(blockIdx.x) % prm.team;
       w.c0 = lo > first ? lo - first : 0;
       w.n = hi - first - w.c0;
       hi = first + w.c0;
@@ -329,7 +332,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     if (tid < p.B) {
       int s_, n_;
       linear_item(p, tid, s_, L, n_);
-      before[tid + 1] = (L + kLpChunk - 1) / kLpChunk * (p.H_v * prm.slices);
+      before[tid + 1] = (L + kLpChunk - 1) / kLpChunk * (p.H_v * prm.slices / prm.team);
     }
     if (tid == 0) before[0] = 0;
     __syncthreads();
@@ -347,10 +350,11 @@ __global__ void __launch_bounds__(kLpThreads, 1)
       }
     }
     __syncthreads();
-    // equal shares; only the last CTAs' may be short or empty, so that no empty
-    // one stands between two parts of a tile
-    const int all = before[p.B], share = (all - 1) / static_cast<int>(gridDim.x) + 1;
-    const long long lo = static_cast<long long>(share) * blockIdx.x;
+    // equal shares; only the last teams' may be short or empty, so that no empty
+    // one stands between two parts of a unit
+    const int teams = static_cast<int>(gridDim.x) / prm.team;
+    const int all = before[p.B], share = (all - 1) / teams + 1;
+    const long long lo = static_cast<long long>(share) * (blockIdx.x / prm.team);
     walk.lo = lo < all ? static_cast<int>(lo) : all;
     walk.hi = lo + share < all ? static_cast<int>(lo) + share : all;
   } else {
@@ -818,7 +822,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
       {
         const float decay = decay_power(log_decay, w.L < kLpChunk ? w.L : kLpChunk);
         const float* start = prm.starts + 4 * r +
-                             static_cast<size_t>(prm.stream ? blockIdx.x - 1 : blockIdx.x) * DK *
+                             static_cast<size_t>(prm.stream ? blockIdx.x - prm.team : blockIdx.x) * DK *
                                  kLpCols;
         uint8_t* lo_s = smem + (g + kStages - 1) % kStages * Shape::kStageBytes + kBoxes * kLpBox;
         if (w.whole_start) {
@@ -827,7 +831,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         } else if (!prm.stream) {
           lp_grid_wait();  // the scan's results
         } else if (elected) {
-          ok = lp_wait_flag(prm.flags + blockIdx.x - 1);
+          ok = lp_wait_flag(prm.flags + blockIdx.x - prm.team);
           if (!ok) {
             flag_error(kErrConsumerWait);
             *abort_word = 1;
