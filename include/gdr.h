@@ -277,8 +277,8 @@ GDR_API int gdr_linear_attention_decode(const gdr_dims* dims, const gdr_bf16* qu
 /*
  * gdr_linear_attention_prefill - the recurrence of gdr_linear_attention_decode
  * over prompts of any length T >= 1, in chunks of 128 tokens on the tensor
- * cores. Arguments as there, without num_accepted_tokens (all valid tokens are
- * committed).
+ * cores (T <= 8: the kernel of gdr_linear_attention_decode). Arguments as there,
+ * without num_accepted_tokens (all valid tokens are committed).
  *   precision   fp32 sums; the state is carried in fp32 across the whole
  *               prompt and rounded to bf16 once. Inside a chunk the weighted
  *               products of queries and keys and the weighted keys are rounded

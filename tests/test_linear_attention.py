@@ -300,9 +300,9 @@ PREFILL = [
     (5, 40, 40, 300, 64, 64, 6),
     (3, 30, 60, 700, 128, 128, 4),
     (40, 2, 4, 130, 64, 192, 40),
-    (9, 10, 20, 3, 128, 64, 9),
+    (9, 10, 20, 13, 128, 64, 9),
     # and more items than a CTA counts
-    (300, 1, 1, 5, 64, 64, 300),
+    (300, 1, 1, 10, 64, 64, 300),
 ]
 
 
