@@ -156,7 +156,10 @@ int launch_linear_decode(const gdr::LinearParams& p, const gdr_host::Device& dev
     rc = encode_rows_map(p.state_pool, p.D_v, DK, static_cast<long long>(p.pool_size) * p.H_v, DK,
                          &pool_map);
   if (rc != GDR_OK) return rc;
-  // the widest part that still gives every SM GDR_LD_BLOCKS_PER_SM blocks
+  // The widest part that still gives every SM GDR_LD_BLOCKS_PER_SM blocks, as many
+  // as run on it at once. Narrower parts repeat the work on q and k: with 16 the
+  // step of 64 items of 32 heads, 128 x 128, takes 32.9 us against 28.8; with 1 a
+  // single item of 64 heads would leave half of the SMs idle.
   const long long heads = static_cast<long long>(p.B) * p.H_v;
   int cols = Shape::kMaxCols;
   while (cols > 64 && (cols >= 2 * p.D_v ||

@@ -6,12 +6,14 @@
 // takes 2 L multiply-adds. A block owns up to 32 KB of one head's state: it
 // arrives by TMA while the block prepares its tokens, is replaced in place in
 // shared memory, and leaves by TMA. Four blocks an SM keep 128 KB in flight,
-// and HBM bounds the call.
+// and HBM bounds the call: 4.4 GB (512 items of 64 heads, 1 token, 64 x 512) in
+// 670 us, 6.5 TB/s; 290 MB (128 items of 32 heads, 8 tokens, 128 x 128) in 52 us,
+// 5.6 TB/s (46 us with the products left out).
 //
 // The multiply-adds run on mma.sync (m16n8k16, bf16 in, fp32 out), whose
 // operands the 16 x 16 pieces of the tile are anyway after two ldmatrix, at
 // a tenth of the instructions of an fp32 loop (which took 138 us where this
-// takes the 49 us of the traffic, 128 items of 32 heads, 8 tokens, 128 x 128):
+// takes 52, 128 items of 32 heads, 8 tokens, 128 x 128):
 //   S_0^T q      both are bf16 as they are stored, so the products are exact;
 //   sum k v^T    K = 16 holds the 8 weighted keys as bf16 hi and lo parts (16
 //                significant bits) against the 8 values twice; the accumulator

@@ -287,8 +287,8 @@ GDR_API int gdr_linear_attention_decode(const gdr_dims* dims, const gdr_bf16* qu
  *               outputs of the tokens before it in its chunk of 128. Padding
  *               (t >= length) may hold anything.
  *   workspace   device memory of at least the bytes that
- *               gdr_linear_attention_prefill_workspace gives for `dims` (0 for
- *               most calls; NULL is fine then), 16-byte aligned, for this call
+ *               gdr_linear_attention_prefill_workspace gives for `dims` (NULL
+ *               is fine where that is 0), 16-byte aligned, for this call
  *               alone until its work is done: two calls that may run at the
  *               same time, or two captured graphs that may, need one each.
  *               A smaller one returns GDR_ERR_NULL.
@@ -304,9 +304,13 @@ GDR_API int gdr_linear_attention_prefill(const gdr_dims* dims, const gdr_bf16* q
                                          gdr_stream_t stream);
 
 /* Bytes of workspace a call of gdr_linear_attention_prefill with these sizes
- * needs on the current device: more than 0 when there are few heads and items
- * for the device's SMs and the prompt is long (its chunks are then cut into
- * segments that run side by side). Host-only. Returns a gdr_status. */
+ * needs on the current device; they hold the states that one thread block hands
+ * to another. More than 0 when items, heads and columns make more tiles than the
+ * device has SMs (every SM then takes an equal share of the chunks), and when they
+ * make few and the prompt is long (its chunks are then cut into segments that run
+ * side by side). 0 for T <= 8. In the first case the launch is a cooperative one:
+ * all its blocks, one an SM, run at the same time, so it starts once the SMs are
+ * free. Host-only. Returns a gdr_status. */
 GDR_API int gdr_linear_attention_prefill_workspace(const gdr_dims* dims, int64_t* bytes);
 
 /* Code types of the state cache. */
