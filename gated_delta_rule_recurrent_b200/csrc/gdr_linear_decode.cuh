@@ -24,7 +24,8 @@
 //
 // Tokens that are not committed have weight 0 in the state and later tokens
 // none in an output, and their values, which may be infinite, are masked there
-// rather than multiplied by 0.
+// rather than multiplied by 0. A committed infinity may come out of the sum as a
+// NaN: its own lo part is one, and the lo part 0 of a key times it is another.
 #pragma once
 
 #include <cuda.h>

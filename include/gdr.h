@@ -263,7 +263,12 @@ GDR_API int gdr_linear_attention_gate(const void* a, const void* b, const float*
  *   sizes       D_k in {64, 128}, D_v a positive multiple of 64, T in [1, 8],
  *               dims->layout = GDR_LAYOUT_KV (GDR_LAYOUT_VK returns
  *               GDR_ERR_UNSUPPORTED)
- *   precision   fp32 throughout; the state is rounded to bf16 once per call.
+ *   precision   fp32 sums of exact products, but for the committed keys' weighted
+ *               values, of which 16 significant bits reach the state; the state
+ *               is rounded to bf16 once per call
+ *   infinities  where the recurrence puts an infinity into the state, the slot
+ *               may get a NaN; nothing else changes, and tokens that are not
+ *               committed stay out of the state whatever they hold.
  * There are no beta, g and gk. Returns a gdr_status.
  */
 GDR_API int gdr_linear_attention_decode(const gdr_dims* dims, const gdr_bf16* query,
@@ -283,9 +288,9 @@ GDR_API int gdr_linear_attention_decode(const gdr_dims* dims, const gdr_bf16* qu
  *               prompt and rounded to bf16 once. Inside a chunk the weighted
  *               products of queries and keys and the weighted keys are rounded
  *               to bf16; the queries read 16 significant bits of the state.
- *   infinities  an infinity or NaN among an item's valid tokens may reach the
- *               outputs of the tokens before it in its chunk of 128. Padding
- *               (t >= length) may hold anything.
+ *   infinities  as there, and an infinity or NaN among an item's valid tokens
+ *               may reach the outputs of the tokens before it in its chunk of
+ *               128. Padding (t >= length) may hold anything.
  *   workspace   device memory of at least the bytes that
  *               gdr_linear_attention_prefill_workspace gives for `dims` (NULL
  *               is fine where that is 0), 16-byte aligned, for this call

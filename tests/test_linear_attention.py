@@ -279,6 +279,27 @@ def test_infinities_of_tokens_that_are_not_committed_stay_out_of_the_state():
     assert not torch.isfinite(out[0, 0, 4, 5])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("op", ["decode", "prefill"])
+@pytest.mark.parametrize("Dk", [64, 128])
+def test_committed_infinities_stay_in_their_rows_and_columns(op, Dk):
+    """Eight tokens: an infinite value, then an infinite key component, in the head that has
+    them; the slot holds no number exactly where the recurrence has none."""
+    x = draw(1, 2, 2, 8, Dk, 128, 1, seed=11, lengths=[8])
+    x["value"][0, 0, 2, 70] = float("inf")
+    x["key"][0, 0, 5, 9] = float("-inf")
+    with np.errstate(invalid="ignore"):
+        ref = oracle(x)
+    mag = oracle(draw(1, 2, 2, 8, Dk, 128, 1, seed=11, lengths=[8]), absolute=True)
+    out, pool = call({k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()},
+                     op)
+    for got, want, m in ((f64(out), ref[0], mag[0]), (f64(pool), ref[1], mag[1])):
+        number = np.isfinite(want)
+        assert not number.all() and np.array_equal(np.isfinite(got), number)
+        got, want, m = got[number], want[number], m[number]
+        assert np.all(np.abs(got - want) <= U * np.abs(want) * 1.01 + 2.0 ** -16 * m)
+
+
 PREFILL = [
     (1, 1, 1, 1, 64, 64, 1),
     (2, 1, 2, 2, 128, 64, 2),
