@@ -46,13 +46,14 @@
 // chain), a small scan turns those into the segments' first states, and the main
 // kernel starts each segment from its own.
 //
-// What bounds it: a chunk takes about 4500 cycles. Its MMAs take 2600 of them and
+// What bounds it: a chunk takes about 4500 cycles (2.5 us; 10 us a call and 1.5 us
+// a further tile of an SM besides; 3.0 us with all SMs at it). Its MMAs take 2600 of them and
 // keep shared memory, where their operands are, about as busy, and three loops
 // are each nearly as long: through the state (its sum, to bf16 tiles, S^T q),
 // through the stage (S^T q, the next load into S_lo's place, q k^T) and through P
 // (q k^T, P, P V). Skipping the work of any one of them gains 1 to 5 %. Measured:
-// the call above 88 us (350 MB, 4.0 TB/s); 4 items of 16 heads, up to 4001 tokens,
-// 64 x 512, 113 us (4.6 TB/s); one item of 8 heads and 32768 tokens 83 us, of which
+// the call above 86 us (350 MB, 4.1 TB/s); 4 items of 16 heads, up to 4001 tokens,
+// 64 x 512, 113 us (4.6 TB/s); one item of 8 heads and 32768 tokens 81 us, of which
 // the first pass is 24 (alone, with cold caches).
 // The loops are kept short in code as well: with all of them unrolled the roles
 // together outgrew the instruction caches (144 us against 103 for the same call).
@@ -289,6 +290,13 @@ __device__ __forceinline__ int lp_piece_offset(int j, int wq, int lane) {
                             32 * wq + 16 * (j & 1) + (lane & 8));
 }
 
+// A tile of a tensor map into L2 (the coordinates of the load that follows).
+__device__ __forceinline__ void lp_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+
 // Set `flag` behind this thread's view of memory; wait for it, bounded.
 __device__ __forceinline__ void lp_set_flag(int* flag) {
   asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(flag), "r"(1) : "memory");
@@ -483,6 +491,14 @@ __global__ void __launch_bounds__(kLpThreads, 1)
           ok = mbar_wait_abandonable(q_free + 8 * st, use ^ 1, abort_word, kErrProducerWait);
           if (!ok) break;
           load(0, &q_map, w.c0 + i, 0, w.qk, kBoxes);
+          // With two stages S_lo leaves k's place just before k is needed: into L2
+          // with it meanwhile (2.49 us a chunk against 2.60). With three the place
+          // is free long before, and the prefetch only costs (2.03 against 2.00).
+          if (kStages == 2) {
+#pragma unroll 1
+            for (int x = 0; x < kBoxes; ++x)
+              lp_prefetch_3d(&k_map, 64 * x, (w.c0 + i) * kLpChunk, w.qk);
+          }
           ok = mbar_wait_abandonable(k_free + 8 * st, k_phase, abort_word, kErrProducerWait);
           if (!ok) break;
           load(1, &k_map, w.c0 + i, 0, w.qk, kBoxes);
