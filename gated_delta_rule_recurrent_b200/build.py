@@ -36,8 +36,8 @@ UNITS = {os.path.join(CSRC, source): [os.path.join(CSRC, name) for name in (sour
          + _COMMON for source, headers in (
     ("gdr_api.cu", ("gdr_decode_tma.cuh", "gdr_decode_chunk.cuh", "gdr_decode_chunk_tc.cuh",
                     "gdr_decode_rows.cuh", "gdr_gate.cuh", "gdr_prefill_tc.cuh")),
-    ("gdr_linear_api.cu", ("gdr_linear.cuh", "gdr_linear_decode.cuh", "gdr_linear_prefill.cuh",
-                           "gdr_state_cache.cuh")))}
+    ("gdr_linear_api.cu", ("gdr_linear.cuh", "gdr_linear_decode.cuh", "gdr_linear_plan.h",
+                           "gdr_linear_prefill.cuh", "gdr_state_cache.cuh")))}
 SOURCES = list(UNITS)
 DEPS = list(dict.fromkeys(path for files in UNITS.values() for path in files))
 OBJ_DIR = os.path.join(PKG_DIR, "_build")

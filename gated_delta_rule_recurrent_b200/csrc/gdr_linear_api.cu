@@ -13,6 +13,7 @@
 #include "gdr.h"
 #include "gdr_host.h"
 #include "gdr_linear_decode.cuh"
+#include "gdr_linear_plan.h"
 #include "gdr_linear_prefill.cuh"
 #include "gdr_state_cache.cuh"
 
@@ -182,54 +183,6 @@ int launch_linear_decode(const gdr::LinearParams& p, const gdr_host::Device& dev
 
 // ---------------------------------------------------------------- prefill
 
-// How a call's chunks are spread over the SMs.
-//   more tiles than SMs: each SM takes an equal share of all chunks (`stream`), in
-//     teams of tiles that read the same q and k;
-//   fewer tiles and long prompts: each tile is cut into `segments`;
-//   else: a CTA for each tile.
-// Cutting costs a pass over k and v and two more launches. With c chunks in n
-// segments, D_k = 128, it took about 23 + 3.8 c / n us where one CTA a tile took
-// 12 + 2.5 c (72 tiles of 16 chunks 55 against 52 us and of 32 chunks 85 against
-// 93 us, n = 2; 36 tiles of 8 chunks 27 against 29 us, n = 4; 4 tiles of 64 chunks
-// 27 against 168 us): it is done where the first is less.
-struct PrefillPlan {
-  int slices = 1, segments = 1, seg_chunks = 1, team = 1, grid = 1;
-  bool stream = false;
-  int64_t states = 0;     // bytes of states in the workspace
-  int64_t workspace = 0;  // and of all of it
-};
-PrefillPlan plan_prefill(const gdr_dims* d, int sms) {
-  PrefillPlan s;
-  if (d->T <= gdr::kMaxT) return s;  // the decode kernel's
-  s.slices = (d->D_v + gdr::kLpCols - 1) / gdr::kLpCols;
-  const int chunks = (d->T - 1) / gdr::kLpChunk + 1;
-  s.seg_chunks = chunks;
-  const long long tiles = static_cast<long long>(d->B) * d->H_v * s.slices;
-  const int64_t state = static_cast<int64_t>(d->D_k) * gdr::kLpCols * 4;
-  s.grid = static_cast<int>(tiles);
-  if (tiles > sms && d->B <= gdr::kLpItems && tiles * chunks < kMaxGrid) {
-    s.stream = true;
-    // tiles that read the same q and k run side by side, up to 8 of them, as long
-    // as teams of that many leave no more than 1 in 16 SMs idle
-    const int sharing = d->H_v / d->H_qk * s.slices;
-    for (int m = 2; m <= 8; ++m)
-      if (sharing % m == 0 && 16 * (sms % m) <= sms) s.team = m;
-    s.grid = sms / s.team * s.team;
-    s.states = s.grid * state;
-    s.workspace = s.states + s.grid * 4;
-    return s;
-  }
-  long long n = sms / tiles;
-  if (n > chunks / 2) n = chunks / 2;
-  if (n >= 2 && chunks * (25 * n - 38) > 110 * n) {
-    s.seg_chunks = static_cast<int>((chunks - 1) / n + 1);
-    s.segments = (chunks - 1) / s.seg_chunks + 1;
-    s.grid = static_cast<int>(tiles) * s.segments;
-    s.states = s.workspace = tiles * s.segments * state;
-  }
-  return s;
-}
-
 // A launch that, with `overlap`, may start before the one ahead of it on the
 // stream is done (the kernel waits for that one where it needs its results), or,
 // with `together`, has all its blocks on the GPU at once (they wait for one
@@ -256,7 +209,7 @@ cudaError_t launch_with(void (*kernel)(P...), int grid, int threads, int smem, b
 }
 
 template <int DK>
-int launch_linear_prefill(const gdr::LinearParams& p, const PrefillPlan& plan, uint8_t* workspace,
+int launch_linear_prefill(const gdr::LinearParams& p, const gdr::PrefillPlan& plan, uint8_t* workspace,
                           const gdr_host::Device& dev, cudaStream_t stream) {
   using Shape = gdr::LpShape<DK>;
   using SegShape = gdr::LsShape<DK>;
@@ -425,7 +378,7 @@ GDR_API int gdr_linear_attention_prefill_workspace(const gdr_dims* dims, int64_t
   gdr_host::Device dev;
   rc = gdr_host::current_device(&dev);
   if (rc != GDR_OK) return rc;
-  *bytes = plan_prefill(dims, dev.sms).workspace;
+  *bytes = gdr::plan_prefill(dims, dev.sms).workspace;
   return GDR_OK;
 }
 
@@ -448,7 +401,7 @@ GDR_API int gdr_linear_attention_prefill(const gdr_dims* dims, const gdr_bf16* q
   gdr_host::Device dev;
   rc = gdr_host::current_device(&dev);
   if (rc != GDR_OK) return rc;
-  const PrefillPlan plan = plan_prefill(dims, dev.sms);
+  const gdr::PrefillPlan plan = gdr::plan_prefill(dims, dev.sms);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (plan.workspace > 0 && (workspace == nullptr || workspace_bytes < plan.workspace))
     return fail(GDR_ERR_NULL, "workspace is smaller than gdr_linear_attention_prefill_workspace "

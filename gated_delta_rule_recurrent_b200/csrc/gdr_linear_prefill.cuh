@@ -146,11 +146,28 @@ static_assert(sizeof(LpWork) <= 64, "an entry of the ring");
 //     come from HBM once for all of them. The last unit comes first: one that goes
 //     on in the next team's share hands its states over early, and one that began
 //     in the share before comes last, when those have long been there.
+// Callable on the host as well, where the schedule is checked without a GPU.
 struct LpWalk {
   const LinearPrefillParams& prm;
   const int* before;  // stream: chunks of all items ahead of item b
+  int block;          // blockIdx.x
   int lo, hi;
-  __device__ __forceinline__ void next(LpWork& w) {
+  // The CTA's range [lo, hi): of all teams' `all` chunks (stream), or of the chunks
+  // of its tile, whose item has L tokens.
+  __host__ __device__ __forceinline__ void share(int all, int teams) {
+    // equal shares; only the last teams' may be short or empty, so that no empty
+    // one stands between two parts of a unit
+    const int each = (all - 1) / teams + 1;
+    const long long from = static_cast<long long>(each) * (block / prm.team);
+    lo = from < all ? static_cast<int>(from) : all;
+    hi = from + each < all ? static_cast<int>(from) + each : all;
+  }
+  __host__ __device__ __forceinline__ void segment(int L) {
+    const int chunks = (L + kLpChunk - 1) / kLpChunk;
+    lo = block % prm.segments * prm.seg_chunks;
+    hi = lo + prm.seg_chunks < chunks ? lo + prm.seg_chunks : chunks;
+  }
+  __host__ __device__ __forceinline__ void next(LpWork& w) {
     w.n = 0;
     if (hi <= lo) return;
     const LinearParams& p = prm.p;
@@ -169,12 +186,12 @@ struct LpWalk {
       chunks = (before[b0 + 1] - before[b0]) / per_item;
       const int in_item = (hi - 1 - before[b0]) / chunks;
       const int first = before[b0] + in_item * chunks;
-      tile = (b0 * per_item + in_item) * prm.team + static_cast<int>(blockIdx.x) % prm.team;
+      tile = (b0 * per_item + in_item) * prm.team + block % prm.team;
       w.c0 = lo > first ? lo - first : 0;
       w.n = hi - first - w.c0;
       hi = first + w.c0;
     } else {
-      tile = static_cast<int>(blockIdx.x) / prm.segments;
+      tile = block / prm.segments;
       w.c0 = lo;
       w.n = hi - lo;
       hi = lo;
@@ -351,7 +368,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
   volatile int* abort_word = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   // this CTA's stretches
-  LpWalk walk{prm, before, 0, 0};
+  LpWalk walk{prm, before, static_cast<int>(blockIdx.x), 0, 0};
   if (prm.stream) {
     int L = 0;
     if (tid < p.B) {
@@ -375,20 +392,11 @@ __global__ void __launch_bounds__(kLpThreads, 1)
       }
     }
     __syncthreads();
-    // equal shares; only the last teams' may be short or empty, so that no empty
-    // one stands between two parts of a unit
-    const int teams = static_cast<int>(gridDim.x) / prm.team;
-    const int all = before[p.B], share = (all - 1) / teams + 1;
-    const long long lo = static_cast<long long>(share) * (blockIdx.x / prm.team);
-    walk.lo = lo < all ? static_cast<int>(lo) : all;
-    walk.hi = lo + share < all ? static_cast<int>(lo) + share : all;
+    walk.share(before[p.B], static_cast<int>(gridDim.x) / prm.team);
   } else {
-    const int tile = blockIdx.x / prm.segments, seg = blockIdx.x % prm.segments;
     int s_, L, n_;
-    linear_item(p, tile / prm.slices / p.H_v, s_, L, n_);
-    const int chunks = (L + kLpChunk - 1) / kLpChunk;
-    walk.lo = seg * prm.seg_chunks;
-    walk.hi = walk.lo + prm.seg_chunks < chunks ? walk.lo + prm.seg_chunks : chunks;
+    linear_item(p, blockIdx.x / prm.segments / prm.slices / p.H_v, s_, L, n_);
+    walk.segment(L);
   }
   LpWork w{};
   // The next stretch from the ring, for the lanes of a warp together; false at the
@@ -864,6 +872,9 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         } else if (!prm.stream) {
           lp_grid_wait();  // the scan's results
         } else if (elected) {
+          // S_lo goes to the k stage that the stretch before left its slot's tile in:
+          // the vote below lets nobody write there until that store has read it
+          bulk_wait_read_all();
           ok = lp_wait_flag(prm.flags + blockIdx.x - prm.team);
           if (!ok) {
             flag_error(kErrConsumerWait);
