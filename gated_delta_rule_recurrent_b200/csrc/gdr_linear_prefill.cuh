@@ -117,7 +117,8 @@ struct LinearPrefillParams {
   // States between CTAs, [D_k / 4][128 columns][4 rows] each (four rows of a column
   // are one 16-byte access, coalesced over the columns). With segments
   // [tiles][segments]: entry g >= 1 is the sum of segment g - 1 after the first
-  // pass, the first state of segment g after the scan. With stream [CTAs]: what CTA
+  // pass, and every entry the first state of its segment after the scan (of items of
+  // several segments). With stream [CTAs]: what CTA
   // c hands to CTA c + team, which may read it once flags[c] is set.
   float* starts;
   int* flags;
@@ -206,8 +207,10 @@ struct LpWalk {
     linear_item(p, b, s, L, n);
     w.slot_row = s * p.H_v + w.h;
     w.L = L - w.c0 * kLpChunk;
-    w.whole_start = w.c0 == 0;
     w.whole_end = w.n * kLpChunk >= w.L;
+    // nothing orders the load of a slot by a tile's first segment and the store by its
+    // last one: several segments all start from the scan's results
+    w.whole_start = w.c0 == 0 && (prm.segments == 1 || w.whole_end);
     w.log_decay = p.log_decay[w.h];
     w.rest = hi;
   }
@@ -1217,8 +1220,8 @@ __global__ void __launch_bounds__(kLsThreads, 1)
 }
 
 // The scan: entry g of prm.starts from the sum of segment g - 1 to the first
-// state of segment g,  start_g = lambda^{segment} start_{g-1} + sum_{g-1}, with
-// start_0 the slot. A thread takes one state value of one tile.
+// state of segment g,  start_g = lambda^{segment} start_{g-1} + sum_{g-1}, and
+// entry 0 to start_0, the slot. A thread takes one state value of one tile.
 constexpr int kLscanThreads = 256;
 template <int DK>
 __global__ void __launch_bounds__(kLscanThreads) linear_scan_kernel(const LinearPrefillParams prm) {
@@ -1243,6 +1246,7 @@ __global__ void __launch_bounds__(kLscanThreads) linear_scan_kernel(const Linear
   if (col < p.D_v)
     x = bf16_bits_to_f32(
         p.state_pool[((static_cast<size_t>(s) * p.H_v + h) * DK + row) * p.D_v + col]);
+  *at = x;
 #pragma unroll 4
   for (int g = 1; g < count; ++g) {
     float* here = at + static_cast<size_t>(g) * DK * kLpCols;

@@ -90,7 +90,10 @@ def check(plan, stretches, shape, lengths):
     B, Hq, Hv, T, Dk, Dv, P = shape
     tiles = collections.defaultdict(list)
     for s in stretches:
-        assert s.n > 0 and s.whole_start == (s.c0 == 0)
+        # from the slot: a tile's first stretch; of a tile in segments only where the block
+        # has all of it, since nothing orders its load and another block's store
+        assert s.n > 0
+        assert s.whole_start == (s.c0 == 0 and (plan.segments == 1 or bool(s.whole_end)))
         tiles[s.bh, s.col0].append(s)
     for b, L in enumerate(lengths):
         L = min(max(L, 0), T)
@@ -124,6 +127,7 @@ CASES = SKEWED + CHAINS + [
     ((300, 1, 1, 10, 64, 64, 300), [10] * 300),
     ((2, 1, 2, 1700, 128, 192, 3), [1700, 900]),
     ((1, 8, 8, 32768, 128, 128, 2), [32768]),
+    ((3, 1, 1, 2900, 64, 320, 3), [2900, 90, 0]),
 ]
 
 
