@@ -403,13 +403,19 @@ __global__ void __launch_bounds__(kLpThreads, 1)
   }
   LpWork w{};
   // The next stretch from the ring, for the lanes of a warp together; false at the
-  // end, or when it did not come.
+  // end, or when it did not come. A group of warps votes on it: one of them may
+  // give up where the others were just let through.
   int n_works = 0;
   const auto next_work = [&]() {
     const int e = n_works % kLpWorks;
-    const bool ok =
+    bool ok =
         __all_sync(0xffffffffu, mbar_wait_abandonable(work_full + 8 * e, (n_works / kLpWorks) & 1,
                                                       abort_word, kErrConsumerWait));
+    if (n_works == 1 && test_give_up(static_cast<int>(blockIdx.x), warp, 0)) {
+      flag_error(kErrConsumerWait);
+      *abort_word = 1;
+      ok = false;
+    }
     if (!ok) return false;
     w = works[e];
     __syncwarp();
@@ -704,9 +710,9 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     const uint32_t base = tmem + kLpTmemP + (static_cast<uint32_t>(32 * wq) << 16);
     bool ok = true;
     int g = 0;
-    while (ok && next_work()) {
+    // behind the vote the weights of the stretch before are no longer read
+    while (ok && named_barrier_and(1, 128, next_work())) {
       const float log_decay = w.log_decay;
-      named_barrier(1, 128);  // the weights of the stretch before are no longer read
       if (wq == 0) diag[lane] = decay_power(log_decay, lane);
       named_barrier(1, 128);
       unsigned long long w2[16];  // lambda^{31-e}
@@ -766,7 +772,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     int leaving = -1;  // the v stage that an output is leaving
     bool ok = true;
     int g = 0;
-    while (ok && next_work()) {
+    while (ok && named_barrier_and(2, 128, next_work())) {
       const float inter = decay_power(w.log_decay, t + 1);
       const unsigned long long inter2 = pk(inter, inter);
       for (int i = 0; i < w.n; ++i, ++g) {
@@ -852,13 +858,15 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     // or two later, when its writes are done and the fence need not wait for them
     // (5000 cycles).
     bool hands = false;
-    const auto pass_on = [&]() {
+    // Every warp comes here once for a state, also one that gave up before (the
+    // state then stays here): none is left alone at the barrier.
+    const auto pass_on = [&](bool good) {
       __threadfence();
-      if (named_barrier_and(3, 128, true) && elected) lp_set_flag(prm.flags + blockIdx.x);
+      if (named_barrier_and(3, 128, good) && elected) lp_set_flag(prm.flags + blockIdx.x);
       hands = false;
     };
     int g = 0;
-    while (ok && next_work()) {
+    while (ok && named_barrier_and(3, 128, next_work())) {
       const float log_decay = w.log_decay;
       // the first state, scaled, into TMEM for the first sum; one that comes from
       // another CTA as hi and lo for its first S^T q too (a slot's tile serves that
@@ -959,6 +967,11 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         // the sum is done and has read this chunk's k: its stage takes S_lo
         ok = __all_sync(0xffffffffu,
                         mbar_wait_abandonable(s_raw, g & 1, abort_word, kErrConsumerWait));
+        if (hands && i == 1 && test_give_up(static_cast<int>(blockIdx.x), warp, 1)) {
+          flag_error(kErrConsumerWait);
+          *abort_word = 1;
+          ok = false;
+        }
         if (!ok) break;
         tc_fence_after();
         if (i + 1 == w.n) {
@@ -989,9 +1002,9 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         fence_async_smem();
         tc_fence_before();
         mbar_arrive(s_ready);
-        if (hands && i > 0) pass_on();
+        if (hands && i > 0) pass_on(true);
       }
-      if (ok && hands) pass_on();
+      if (hands) pass_on(ok);
       // The stretch's last state: rounded once to the slot, through a tile in the
       // last chunk's k stage (two-byte stores to the slot itself took 8000 cycles), or
       // as it is to the next CTA. With segments the next one has its state from the
@@ -1034,7 +1047,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         bulk_commit_group();
       }
     }
-    if (ok && hands) pass_on();
+    if (ok && hands) pass_on(true);
     if (elected) bulk_wait_all();
   }
 

@@ -37,9 +37,18 @@ __device__ __forceinline__ long long abandonable_wait_limit() {
 __device__ __forceinline__ bool test_hold_tile(int tile) {
   return tile == *reinterpret_cast<volatile int*>(&g_test_hold_tile);
 }
+// With a negative "tile", one warp of a block of 16 gives up at a place of the linear
+// prefill kernel instead, alone and while the others go on: -2 - (2 (16 block + warp)
+// + place), place 0 as it takes its second stretch of chunks, 1 behind the sum of a
+// stretch's second chunk while a state is still to be handed on.
+__device__ __forceinline__ bool test_give_up(int block, int warp, int place) {
+  return -2 - (2 * (16 * block + warp) + place) ==
+         *reinterpret_cast<volatile int*>(&g_test_hold_tile);
+}
 #else
 __device__ __forceinline__ constexpr long long abandonable_wait_limit() { return kWaitLimitCycles; }
 __device__ __forceinline__ constexpr bool test_hold_tile(int) { return false; }
+__device__ __forceinline__ constexpr bool test_give_up(int, int, int) { return false; }
 #endif
 
 // Byte offset of (row i, 16-byte chunk holding column col) in a state tile
