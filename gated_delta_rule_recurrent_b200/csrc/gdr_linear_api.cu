@@ -237,10 +237,10 @@ int launch_linear_prefill(const gdr::LinearParams& p, const gdr::PrefillPlan& pl
   prm.segments = plan.segments;
   prm.seg_chunks = plan.seg_chunks;
   prm.starts = reinterpret_cast<float*>(workspace);
+  prm.flags = reinterpret_cast<int*>(workspace + plan.states);
   const int tiles = p.B * p.H_v * plan.slices;
   cudaError_t err = cudaSuccess;
   if (plan.stream) {
-    prm.flags = reinterpret_cast<int*>(workspace + plan.states);
     err = cudaMemsetAsync(prm.flags, 0, static_cast<size_t>(plan.grid) * 4, stream);
   } else if (plan.segments > 1) {
     seg_kernel<<<tiles * (plan.segments - 1), gdr::kLsThreads, SegShape::kSmem, stream>>>(

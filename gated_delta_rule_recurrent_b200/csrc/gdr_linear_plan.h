@@ -53,7 +53,8 @@ inline PrefillPlan plan_prefill(const gdr_dims* d, int sms) {
     s.seg_chunks = static_cast<int>((chunks - 1) / n + 1);
     s.segments = (chunks - 1) / s.seg_chunks + 1;
     s.grid = static_cast<int>(tiles) * s.segments;
-    s.states = s.workspace = tiles * s.segments * state;
+    s.states = s.grid * state;
+    s.workspace = s.states + s.grid * 4;
   }
   return s;
 }

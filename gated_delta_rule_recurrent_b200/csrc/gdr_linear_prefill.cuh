@@ -121,6 +121,8 @@ struct LinearPrefillParams {
   // several segments). With stream [CTAs]: what CTA
   // c hands to CTA c + team, which may read it once flags[c] is set.
   float* starts;
+  // With stream [CTAs], see above. With segments [tiles][segments]: entry g >= 1 says
+  // whether the first pass got to the end of the sum of segment g - 1.
   int* flags;
 };
 
@@ -868,6 +870,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     int g = 0;
     while (ok && named_barrier_and(3, 128, next_work())) {
       const float log_decay = w.log_decay;
+      bool sums = true;  // segments: what this thread looked up of the sums behind its start
       // the first state, scaled, into TMEM for the first sum; one that comes from
       // another CTA as hi and lo for its first S^T q too (a slot's tile serves that
       // as it is)
@@ -882,6 +885,8 @@ __global__ void __launch_bounds__(kLpThreads, 1)
           ++slots;
         } else if (!prm.stream) {
           lp_grid_wait();  // the scan's results
+          for (int e = r; e < static_cast<int>(blockIdx.x) % prm.segments; e += 128)
+            sums = sums && __ldcg(prm.flags + blockIdx.x - e) != 0;
         } else if (elected) {
           // S_lo goes to the k stage that the stretch before left its slot's tile in:
           // the vote below lets nobody write there until that store has read it
@@ -1038,7 +1043,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         }
       }
       fence_async_smem();
-      ok = named_barrier_and(3, 128, ok);
+      ok = named_barrier_and(3, 128, ok && sums);  // no slot from a sum that is not there
       hands = ok && prm.stream && !w.whole_end;
       if (ok && w.whole_end && elected) {
         for (int x = 0; x < w.cols / 64; ++x)
@@ -1067,7 +1072,8 @@ __global__ void __launch_bounds__(kLpThreads, 1)
 // prm.seg_chunks whole chunks:  sum_j lambda^{end-1-j} k_j v_j^T  over its
 // tokens j, into the next segment's entry of prm.starts as [D_k][128 columns]
 // fp32. The weights reach from the segment's end, so the chunks' products add
-// up in TMEM and nothing waits for the state. 64 KB a chunk at D_k = 128: HBM
+// up in TMEM and nothing waits for the state. Every block says in prm.flags whether
+// its sum is there; without one the item's slot is not written. 64 KB a chunk at D_k = 128: HBM
 // bounds it once the segments fill the SMs.
 template <int DK>
 struct LsShape {
@@ -1140,9 +1146,13 @@ __global__ void __launch_bounds__(kLsThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  // the test hook counts these blocks on from the main kernel's
+  const bool loads = !test_hold_tile(
+      static_cast<int>(gridDim.x / (prm.segments - 1) * prm.segments + blockIdx.x));
+  bool stored = true;
   if (warp == 4) {
     // ------------------------------------------------------------ load
-    if (lane == 0) {
+    if (lane == 0 && loads) {
       const int zk = b * p.H_qk + h / p.group;
       int issued = 0;
       for (int i = 0; i < n_chunks; ++i) {
@@ -1204,7 +1214,8 @@ __global__ void __launch_bounds__(kLsThreads, 1)
       mbar_arrive(ready + 8 * st);
     }
     ok = ok && mbar_wait_abandonable(summed, 0, abort_word, kErrConsumerWait);
-    if (__all_sync(0xffffffffu, ok)) {
+    stored = __all_sync(0xffffffffu, ok);
+    if (stored) {
       tc_fence_after();
       const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
       float* dst = prm.starts +
@@ -1225,7 +1236,8 @@ __global__ void __launch_bounds__(kLsThreads, 1)
 
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  stored = __syncthreads_and(stored);
+  if (tid == 0) prm.flags[static_cast<size_t>(tile) * prm.segments + seg + 1] = stored;
   if (warp == 4) {
     tc_fence_after();
     tmem_dealloc(tmem, 128);
