@@ -858,7 +858,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     bool ok = true;
     // A state written for the next CTA and not passed on yet: that happens a chunk
     // or two later, when its writes are done and the fence need not wait for them
-    // (5000 cycles).
+    // (5000 cycles); but before this CTA itself waits for another one's state.
     bool hands = false;
     // Every warp comes here once for a state, also one that gave up before (the
     // state then stays here): none is left alone at the barrier.
@@ -875,6 +875,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
       // another CTA as hi and lo for its first S^T q too (a slot's tile serves that
       // as it is)
       {
+        if (hands && !w.whole_start) pass_on(true);
         const float decay = decay_power(log_decay, w.L < kLpChunk ? w.L : kLpChunk);
         const float* start = prm.starts + 4 * r +
                              static_cast<size_t>(prm.stream ? blockIdx.x - prm.team : blockIdx.x) * DK *

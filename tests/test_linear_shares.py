@@ -77,3 +77,21 @@ def test_one_warp_that_gives_up_alone_ends_the_call(hooks, block, warp, place):
     out, word = _hooked_call(hooks, xd, "prefill")
     assert word == 0
     check(x, "prefill", (out, xd["state_pool"]), ref, mag, x["state_pool"])
+
+
+def test_a_state_is_handed_on_before_its_block_waits_for_one(hooks):
+    """With block 0 held back, the one state that does not come is tile 1's: the blocks behind
+    it hand theirs on before they wait, so tiles 2 .. are right (and not a chain in which each
+    block waits for all the ones before it)."""
+    shape, lengths = CHAINS[0]
+    x = draw(*shape, seed=24, lengths=lengths)
+    ref, mag = chain_oracle()
+    xd = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+    assert hooks.gdrtest_set_hooks(4_000_000, 0) == 0
+    _, word = _hooked_call(hooks, xd, "prefill")
+    assert hooks.gdrtest_set_hooks(0, -1) == 0
+    assert word & 3 and not word & 4, word
+    now, was = f64(xd["state_pool"]), f64(x["state_pool"])
+    right = np.abs(now - ref[1]) <= U * np.abs(ref[1]) * 1.01 + (U + 2.0 ** -12) * mag[1]
+    assert (now[0, :2] == was[0, :2]).all()
+    assert right[0, 2:].all()
