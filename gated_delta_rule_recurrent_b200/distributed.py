@@ -24,7 +24,8 @@ import torch.distributed as dist
 __all__ = ["rank_env", "rank_seed", "max_over_ranks", "sum_over_ranks", "throughput",
            "Shard", "shard_bounds", "shard_call", "gather_call"]
 
-# Argument names of one call (the op page's, plus the fused gate's inputs).
+# Argument names of one call (the op page's, plus the fused gate's inputs) with items on
+# axis 0. Linear attention's log_decay, like the gate's vectors, is [H_v].
 _ITEM_AXIS0 = ("query", "key", "value", "beta", "g", "gk", "a", "b", "actual_seq_lengths",
                "ssm_state_indices", "num_accepted_tokens")
 
@@ -100,7 +101,7 @@ def shard_call(x: Dict[str, object], world: int, rank: int,
         for k in ("a", "b"):  # [B, T, H_v]: heads last
             if x.get(k) is not None:
                 out[k] = x[k][:, :, lo:hi].contiguous()
-        for k in ("dt_bias", "decay_scale"):
+        for k in ("dt_bias", "decay_scale", "log_decay"):  # [H_v]
             if x.get(k) is not None:
                 out[k] = x[k][lo:hi].contiguous()
         out["state_pool"] = pool[:, lo:hi].contiguous()
