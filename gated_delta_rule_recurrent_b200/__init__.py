@@ -21,10 +21,13 @@ _LAZY = {"decode", "decode_gated", "prefill", "prefill_gated", "linear_attention
          "last_launch", "kernel_forms"}
 
 
-def __getattr__(name):
-    if name in _LAZY:
-        from . import binding
+_binding = None  # the module behind the names, once it is loaded
 
-        value = globals()[name] = getattr(binding, name)  # found directly from now on
-        return value
+
+def __getattr__(name):
+    global _binding
+    if name in _LAZY:
+        if _binding is None:
+            from . import binding as _binding
+        return getattr(_binding, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
