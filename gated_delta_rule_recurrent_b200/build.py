@@ -85,6 +85,13 @@ def _run(cmd, verbose: bool) -> None:
         print(res.stdout + res.stderr, flush=True)
 
 
+def _forget(path) -> None:
+    """Remove the sidecar file of something that is about to be written again: an
+    interruption in between must not leave the old hash beside the new file."""
+    if os.path.exists(path + ".srchash"):
+        os.remove(path + ".srchash")
+
+
 def build(verbose: bool = False, extra=(), test_hooks: bool = False, reuse: bool = False) -> str:
     """Compile every source, side by side, and link the library. With ``reuse``
     an object whose sources and flags are unchanged is not compiled again."""
@@ -100,6 +107,7 @@ def build(verbose: bool = False, extra=(), test_hooks: bool = False, reuse: bool
             with open(obj + ".srchash") as f:
                 if f.read().strip() == key:
                     return obj
+        _forget(obj)
         _run(compile_command(source, obj, [*flags, *extra]), verbose)
         with open(obj + ".srchash", "w") as f:
             f.write(key + "\n")
@@ -107,6 +115,7 @@ def build(verbose: bool = False, extra=(), test_hooks: bool = False, reuse: bool
 
     with concurrent.futures.ThreadPoolExecutor(len(UNITS)) as pool:
         objs = list(pool.map(one, UNITS))
+    _forget(out)
     _run(link_command(objs, out), verbose)
     with open(out + ".srchash", "w") as f:
         f.write(source_hash(flags) + "\n")
