@@ -24,11 +24,18 @@ namespace {
 constexpr int kMaxDevices = 64;
 constexpr long long kMaxGrid = 0x7fffffffLL;
 
+// A runtime call that failed: its status, and nothing left of the error for the
+// next launch to take for its own.
+int cuda_failed(const std::string& what, cudaError_t err) {
+  (void)cudaGetLastError();
+  return fail(GDR_ERR_CUDA, what + ": " + cudaGetErrorString(err));
+}
+
 int launched(const char* what, int kernel, int D_k, int tile_cols, int layout, int grid,
              int threads, int smem, int stages) {
   const cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess)
-    return fail(GDR_ERR_CUDA, std::string(what) + " launch failed: " + cudaGetErrorString(err));
+    return cuda_failed(std::string(what) + " launch failed", err);
   gdr_host::set_last_launch(
       gdr_launch_info{kernel, D_k, tile_cols, 0, layout, grid, threads, smem, stages});
   return GDR_OK;
@@ -134,7 +141,7 @@ int opt_in_smem(K kernel, int smem, const gdr_host::Device& dev, std::atomic<boo
     err = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                                cudaSharedmemCarveoutMaxShared);
   if (err != cudaSuccess)
-    return fail(GDR_ERR_CUDA, std::string("kernel attributes: ") + cudaGetErrorString(err));
+    return cuda_failed("kernel attributes", err);
   ready[dev.ordinal].store(true, std::memory_order_release);
   return GDR_OK;
 }
@@ -255,7 +262,7 @@ int launch_linear_prefill(const gdr::LinearParams& p, const gdr::PrefillPlan& pl
     err = launch_with(kernel, plan.grid, gdr::kLpThreads, Shape::kSmem, plan.segments > 1,
                       plan.stream, stream, q_map, k_map, v_map, o_map, pool_map, prm);
   if (err != cudaSuccess)
-    return fail(GDR_ERR_CUDA, std::string("linear prefill launch: ") + cudaGetErrorString(err));
+    return cuda_failed("linear prefill launch", err);
   return launched("linear prefill", GDR_KERNEL_LINEAR_PREFILL, DK, gdr::kLpCols, GDR_LAYOUT_KV,
                   plan.grid, gdr::kLpThreads, Shape::kSmem, Shape::kStages);
 }
