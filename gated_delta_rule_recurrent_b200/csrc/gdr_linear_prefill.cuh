@@ -1107,14 +1107,8 @@ __global__ void __launch_bounds__(kLsThreads, 1)
   lp_grid_launch_next();
   const int64_t end = static_cast<int64_t>(seg + 1) * prm.seg_chunks * kLpChunk;
   if (L <= end) return;  // the item's last segment, or behind it
-  // chunks whose weights are all 0 in fp32 add nothing: start behind them
   const float log_decay = p.log_decay[h];
-  int skip = 0;
-  while (skip < prm.seg_chunks - 1 &&
-         decay_power(log_decay, (prm.seg_chunks - 1 - skip) * kLpChunk) == 0.0f)
-    ++skip;
-  const int c0 = seg * prm.seg_chunks + skip;
-  const int n_chunks = prm.seg_chunks - skip;
+  const int c0 = seg * prm.seg_chunks, n_chunks = prm.seg_chunks;
 
   extern __shared__ __align__(16) uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
