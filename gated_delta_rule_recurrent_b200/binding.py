@@ -493,8 +493,9 @@ def linear_attention_prefill(query: torch.Tensor, key: torch.Tensor, value: torc
                              ) -> Tuple[torch.Tensor, torch.Tensor]:
     """The recurrence of ``linear_attention_decode`` over prompts of any length,
     through ``gdr_linear_attention_prefill`` (chunks of 128 tokens on the tensor
-    cores). All valid tokens are committed. Queued on the current CUDA stream;
-    no synchronisation.
+    cores). All valid tokens are committed. An infinity or NaN in a valid token's
+    value may reach its column of the outputs of the tokens before it in its chunk.
+    Queued on the current CUDA stream; no synchronisation.
     """
     index, dims, out = _linear_args(query, key, value, log_decay, state_pool,
                                     actual_seq_lengths, ssm_state_indices, None, out)

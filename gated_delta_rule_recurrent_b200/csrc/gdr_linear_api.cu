@@ -148,9 +148,7 @@ int opt_in_smem(K kernel, int smem, const gdr_host::Device& dev, std::atomic<boo
 
 // ---------------------------------------------------------------- decode
 
-#ifndef GDR_LD_BLOCKS_PER_SM
-#define GDR_LD_BLOCKS_PER_SM 4
-#endif
+constexpr int kLdBlocksPerSm = 4;
 
 template <int DK>
 int launch_linear_decode(const gdr::LinearParams& p, const gdr_host::Device& dev,
@@ -164,15 +162,15 @@ int launch_linear_decode(const gdr::LinearParams& p, const gdr_host::Device& dev
     rc = encode_rows_map(p.state_pool, p.D_v, DK, static_cast<long long>(p.pool_size) * p.H_v, DK,
                          &pool_map);
   if (rc != GDR_OK) return rc;
-  // The widest part that still gives every SM GDR_LD_BLOCKS_PER_SM blocks, as many
-  // as run on it at once. Narrower parts repeat the work on q and k: with 16 the
-  // step of 64 items of 32 heads, 128 x 128, takes 32.9 us against 28.8; with 1 a
-  // single item of 64 heads would leave half of the SMs idle.
+  // The widest part that still gives every SM kLdBlocksPerSm blocks, as many as run
+  // on it at once. Narrower parts repeat the work on q and k: with 16 the step of 64
+  // items of 32 heads, 128 x 128, takes 32.9 us against 28.8; with 1 a single item of
+  // 64 heads would leave half of the SMs idle.
   const long long heads = static_cast<long long>(p.B) * p.H_v;
   int cols = Shape::kMaxCols;
   while (cols > 64 && (cols >= 2 * p.D_v ||
                        heads * ((p.D_v - 1) / cols + 1) <
-                           static_cast<long long>(GDR_LD_BLOCKS_PER_SM) * dev.sms))
+                           static_cast<long long>(kLdBlocksPerSm) * dev.sms))
     cols /= 2;
   const int parts = (p.D_v - 1) / cols + 1;
   const int grid = static_cast<int>(heads) * parts;
@@ -303,10 +301,8 @@ int check_cache(const void* pool, int32_t pool_size, const int32_t* slots, const
 }
 
 // Launches the form of a cache kernel that fits the call: 8 pieces a lane where
-// that still gives every SM GDR_CACHE_BLOCKS_PER_SM blocks.
-#ifndef GDR_CACHE_BLOCKS_PER_SM
-#define GDR_CACHE_BLOCKS_PER_SM 8
-#endif
+// that still gives every SM kCacheBlocksPerSm blocks.
+constexpr int kCacheBlocksPerSm = 8;
 template <typename K>
 int launch_cache(K many, K few, const char* what, gdr::CacheParams p, int n,
                  gdr_stream_t stream) {
@@ -316,7 +312,7 @@ int launch_cache(K many, K few, const char* what, gdr::CacheParams p, int n,
   const auto blocks = [&](int ahead) {
     return (p.slot_values - 1) / (gdr::kCacheThreads * ahead * 8) + 1;
   };
-  const bool is_few = blocks(gdr::kCacheAhead) * n < GDR_CACHE_BLOCKS_PER_SM * dev.sms;
+  const bool is_few = blocks(gdr::kCacheAhead) * n < kCacheBlocksPerSm * dev.sms;
   p.blocks_per_slot =
       static_cast<int>(blocks(is_few ? gdr::kCacheAheadFew : gdr::kCacheAhead));
   const int grid = n * p.blocks_per_slot;

@@ -7,8 +7,8 @@
 // arrives by TMA while the block prepares its tokens, is replaced in place in
 // shared memory, and leaves by TMA. Four blocks an SM keep 128 KB in flight,
 // and HBM bounds the call: 4.4 GB (512 items of 64 heads, 1 token, 64 x 512) in
-// 670 us, 6.5 TB/s; 290 MB (128 items of 32 heads, 8 tokens, 128 x 128) in 52 us,
-// 5.6 TB/s (46 us with the products left out).
+// 670 to 731 us by the GPU, 6.0 to 6.5 TB/s; 290 MB (128 items of 32 heads, 8
+// tokens, 128 x 128) in 52 us, 5.6 TB/s (46 us with the products left out).
 //
 // The multiply-adds run on mma.sync (m16n8k16, bf16 in, fp32 out), whose
 // operands the 16 x 16 pieces of the tile are anyway after two ldmatrix, at
@@ -107,7 +107,7 @@ __device__ __forceinline__ bool mbar_wait_abandonable_alone(uint32_t bar, uint32
 }
 
 // Blocks an SM: 5 where the registers decide (512 items of 64 heads, 64 x 512:
-// 670 us against 679 for 4); at D_k = 128 shared memory leaves room for 4, and
+// 670 us against 679 for 4 on one GPU); at D_k = 128 shared memory leaves room for 4, and
 // the registers of 4 are faster (8 tokens, 128 x 128: 52 us against 55).
 template <int DK>
 __global__ void __launch_bounds__(kLdThreads, DK == 128 ? 4 : 5)

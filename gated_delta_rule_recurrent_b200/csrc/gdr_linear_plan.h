@@ -15,11 +15,18 @@ namespace gdr {
 //     teams of tiles that read the same q and k;
 //   fewer tiles and long prompts: each tile is cut into `segments`;
 //   else: a CTA for each tile.
-// Cutting costs a pass over k and v and two more launches. With c chunks in n
-// segments, D_k = 128, it took about 23 + 3.8 c / n us where one CTA a tile took
-// 12 + 2.5 c (72 tiles of 16 chunks 55 against 52 us and of 32 chunks 85 against
-// 93 us, n = 2; 36 tiles of 8 chunks 27 against 29 us, n = 4; 4 tiles of 64 chunks
-// 27 against 168 us): it is done where the first is less.
+// Cutting costs a pass over k and v and two more launches. The rule is a fit at
+// D_k = 128 (c chunks in n segments: about 23 + 3.8 c / n us against 12 + 2.5 c) and
+// serves D_k = 64 too. Cut against whole, cold caches, us, around its border:
+//   tiles x chunks   72 x 16  72 x 24  72 x 32  48 x 12  36 x 8  36 x 12  4 x 6  4 x 64
+//   n                2        2        2        3        4       4        3      32
+//   D_k = 128, cut   60       75       89       42       34      38       26     32
+//              whole 53       72       90       41       31      41       25     158
+//   D_k = 64, cut    46       58       71       34       28      32       20     28
+//             whole  45       60       77       35       27      35       23     135
+//   cut?             no       yes      yes      yes      yes     yes      no     yes
+// so that near the border the wrong side costs up to a tenth, and far from it none is
+// taken.
 struct PrefillPlan {
   int slices = 1, segments = 1, seg_chunks = 1, team = 1, grid = 1;
   bool stream = false;

@@ -39,7 +39,12 @@
 //
 // Many tiles: lengths differ, and tiles rarely fill the last wave of SMs, so with
 // more tiles than SMs every SM takes an equal share of all chunks instead of whole
-// tiles (8 items of 32 heads, up to 2048 tokens, 128 x 128: 94 us against 100).
+// tiles (8 items of 32 heads, up to 2048 tokens, 128 x 128: 94 us against 100 at the
+// step that brought it). A tile that goes on in the next share hands its state to that
+// CTA; a CTA hands its own on before it waits for another one's, so that only the
+// chunks of one tile follow one another (128 x 128: 150 heads of 8192 tokens, 64
+// chunks each, 207 us against 654 with the state held back until then; one prompt of
+// 16384 tokens among seven of 256, 32 heads, 430 us against 4019: 128 chunks in a row).
 // Long prompts of few heads: the chunks of a tile are cut into segments of a CTA
 // each, where that is faster. A first pass sums each segment's
 // sum_j lambda^{end-1-j} k_j v_j^T (half the operands, one product a chunk, no
@@ -52,9 +57,10 @@
 // are each nearly as long: through the state (its sum, to bf16 tiles, S^T q),
 // through the stage (S^T q, the next load into S_lo's place, q k^T) and through P
 // (q k^T, P, P V). Skipping the work of any one of them gains 1 to 5 %. Measured:
-// the call above 86 us (350 MB, 4.1 TB/s); 4 items of 16 heads, up to 4001 tokens,
-// 64 x 512, 113 us (4.6 TB/s); one item of 8 heads and 32768 tokens 81 us, of which
-// the first pass is 24 (alone, with cold caches).
+// the call above 84 to 104 us by the draw of its lengths (350 MB in 93 us, 3.8 TB/s);
+// 4 items of 16 heads, up to 4001 tokens, 64 x 512, 117 to 139 us (4.2 TB/s); one item
+// of 8 heads and 32768 tokens 93 to 96 us (2.8 TB/s), of which the first pass is 28
+// (alone, with cold caches).
 // The loops are kept short in code as well: with all of them unrolled the roles
 // together outgrew the instruction caches (144 us against 103 for the same call).
 //
@@ -1071,8 +1077,9 @@ __global__ void __launch_bounds__(kLpThreads, 1)
 
 // First pass: the sum of a segment that another one follows, which is
 // prm.seg_chunks whole chunks:  sum_j lambda^{end-1-j} k_j v_j^T  over its
-// tokens j, into the next segment's entry of prm.starts as [D_k][128 columns]
-// fp32. The weights reach from the segment's end, so the chunks' products add
+// tokens j, into the next segment's entry of prm.starts (fp32, laid out as it says
+// there). Chunks whose weights are 0 in fp32 are summed like the others: 0 times an
+// infinity or NaN is none (without them the call above took 3 to 6 us less). The weights reach from the segment's end, so the chunks' products add
 // up in TMEM and nothing waits for the state. Every block says in prm.flags whether
 // its sum is there; without one the item's slot is not written. 64 KB a chunk at D_k = 128: HBM
 // bounds it once the segments fill the SMs.

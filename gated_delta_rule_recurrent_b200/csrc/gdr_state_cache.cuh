@@ -15,7 +15,8 @@
 // of one slot (a slot is contiguous whatever its layout, and rows are whole
 // groups in both layouts of the pool). A lane has 8 accesses in flight, 128
 // threads a block: 256 of 512 slots of 64 heads of 64 x 512 written and read
-// back in 500 us (6.6 TB/s; 4 in flight and 256 threads 521 us). Calls too small
+// back in 500 to 542 us by the GPU (6.1 to 6.6 TB/s, the copy rate; 4 in flight and
+// 256 threads 521 us where this took 500). Calls too small
 // to fill the SMs that way take 2 accesses a lane and four times the blocks: one
 // such slot, 8.4 us for both calls against 10.5 us.
 #pragma once

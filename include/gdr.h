@@ -288,9 +288,11 @@ GDR_API int gdr_linear_attention_decode(const gdr_dims* dims, const gdr_bf16* qu
  *               prompt and rounded to bf16 once. Inside a chunk the weighted
  *               products of queries and keys and the weighted keys are rounded
  *               to bf16; the queries read 16 significant bits of the state.
- *   infinities  as there, and an infinity or NaN among an item's valid tokens
- *               may reach the outputs of the tokens before it in its chunk of
- *               128. Padding (t >= length) may hold anything.
+ *   infinities  as there, and an infinity or NaN in a valid token's value may
+ *               reach its column of the outputs of the tokens before it in
+ *               its chunk of 128 (0 times an infinity); those of a key or a
+ *               query reach no token before theirs. Padding (t >= length) may
+ *               hold anything.
  *   workspace   device memory of at least the bytes that
  *               gdr_linear_attention_prefill_workspace gives for `dims` (NULL
  *               is fine where that is 0), 16-byte aligned, for this call
@@ -310,12 +312,13 @@ GDR_API int gdr_linear_attention_prefill(const gdr_dims* dims, const gdr_bf16* q
 
 /* Bytes of workspace a call of gdr_linear_attention_prefill with these sizes
  * needs on the current device; they hold the states that one thread block hands
- * to another. More than 0 when items, heads and columns make more tiles than the
+ * to another, and which of them are there. More than 0 when items, heads and columns make more tiles than the
  * device has SMs (every SM then takes an equal share of the chunks), and when they
  * make few and the prompt is long (its chunks are then cut into segments that run
  * side by side). 0 for T <= 8. In the first case the launch is a cooperative one:
  * all its blocks, one an SM, run at the same time, so it starts once the SMs are
- * free. Host-only. Returns a gdr_status. */
+ * free, and a context with fewer SMs than the device (MPS, a green context) cannot
+ * take it: the call returns GDR_ERR_CUDA there. Host-only. Returns a gdr_status. */
 GDR_API int gdr_linear_attention_prefill_workspace(const gdr_dims* dims, int64_t* bytes);
 
 /* Code types of the state cache. */
