@@ -929,7 +929,7 @@ GDR_API int gdr_abi_version(void) { return 6; }
 #ifdef GDR_TEST_HOOKS
 // Test builds only (libgdr_testhooks.so): shorten the budget of the
 // abandonable waits (cycles; <= 0 restores the shipped ~2 s) and hold back the
-// tile with index `hold_tile` (< 0: none) in every decode kernel. Synchronous.
+// tile with index `hold_tile` (-1: none, below: test_give_up) in every decode kernel. Synchronous.
 // Not part of the library's ABI: the shipped libgdr.so does not contain it.
 GDR_API int gdrtest_set_hooks(long long wait_limit_cycles, int hold_tile) {
   const long long limit = wait_limit_cycles > 0 ? wait_limit_cycles : gdr::kWaitLimitCycles;

@@ -35,7 +35,8 @@ __device__ __forceinline__ float decay_power(float log_decay, int n) {
 
 // Item b's slot s, valid tokens L (0 when the slot is outside the pool) and
 // committed tokens n.
-__host__ __device__ __forceinline__ void linear_item(const LinearParams& p, int b, int& s, int& L, int& n) {
+__host__ __device__ __forceinline__ void linear_item(const LinearParams& p, int b, int& s,
+                                                     int& L, int& n) {
   s = p.state_indices[b];
   L = p.seq_lengths[b];
   L = L < 0 ? 0 : (L > p.T ? p.T : L);

@@ -214,8 +214,9 @@ cudaError_t launch_with(void (*kernel)(P...), int grid, int threads, int smem, b
 }
 
 template <int DK>
-int launch_linear_prefill(const gdr::LinearParams& p, const gdr::PrefillPlan& plan, uint8_t* workspace,
-                          const gdr_host::Device& dev, cudaStream_t stream) {
+int launch_linear_prefill(const gdr::LinearParams& p, const gdr::PrefillPlan& plan,
+                          uint8_t* workspace, const gdr_host::Device& dev,
+                          cudaStream_t stream) {
   using Shape = gdr::LpShape<DK>;
   using SegShape = gdr::LsShape<DK>;
   static std::atomic<bool> ready[kMaxDevices], seg_ready[kMaxDevices];

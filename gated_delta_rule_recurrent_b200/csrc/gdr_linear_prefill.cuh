@@ -124,8 +124,8 @@ struct LinearPrefillParams {
   // are one 16-byte access, coalesced over the columns). With segments
   // [tiles][segments]: entry g >= 1 is the sum of segment g - 1 after the first
   // pass, and every entry the first state of its segment after the scan (of items of
-  // several segments). With stream [CTAs]: what CTA
-  // c hands to CTA c + team, which may read it once flags[c] is set.
+  // several segments). With stream [CTAs]: what CTA c hands to CTA c + team, which may
+  // read it once flags[c] is set.
   float* starts;
   // With stream [CTAs], see above. With segments [tiles][segments]: entry g >= 1 says
   // whether the first pass got to the end of the sum of segment g - 1.
@@ -1078,11 +1078,12 @@ __global__ void __launch_bounds__(kLpThreads, 1)
 // First pass: the sum of a segment that another one follows, which is
 // prm.seg_chunks whole chunks:  sum_j lambda^{end-1-j} k_j v_j^T  over its
 // tokens j, into the next segment's entry of prm.starts (fp32, laid out as it says
-// there). Chunks whose weights are 0 in fp32 are summed like the others: 0 times an
-// infinity or NaN is none (without them the call above took 3 to 6 us less). The weights reach from the segment's end, so the chunks' products add
-// up in TMEM and nothing waits for the state. Every block says in prm.flags whether
-// its sum is there; without one the item's slot is not written. 64 KB a chunk at D_k = 128: HBM
-// bounds it once the segments fill the SMs.
+// there). The weights reach from the segment's end, so the chunks' products add up
+// in TMEM and nothing waits for the state. Chunks whose weights are 0 in fp32 are
+// summed like the others, since 0 times an infinity or NaN is not 0 (leaving them out
+// took 3 to 6 us off the long call above). Every block says in prm.flags whether its
+// sum is there; without one the item's slot is not written. 64 KB a chunk at
+// D_k = 128: HBM bounds it once the segments fill the SMs.
 template <int DK>
 struct LsShape {
   static constexpr int kBoxes = DK / 64;
